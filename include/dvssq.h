@@ -320,6 +320,121 @@ DVSSQ_API dvssq_status dvssq_bss_attention(const dvssq_attn_shape *shape, const 
                                            void *workspace, size_t workspace_bytes,
                                            void *stream);
 
+/* ---------------------------------------------------- 8-bit KV cache ----
+ * A paged KV cache in 8 bits, and KV-BSS decode attention over it.  A row x
+ * (one token and KV head, d values) is held like a row of the salient INT8
+ * tier (Spark card, Tier A), one BF16 scale per row:
+ *   s = RN_bf16(max|x| / 127),  c = clip(rint(x / s), -127, 127)  (0 if s = 0)
+ * and stands for c s.  A row with an infinity or a NaN gets a NaN scale and
+ * reads back as NaN.
+ *
+ * The pool holds n_pages pages of DVSSQ_KV_PAGE tokens each:
+ *   k        int8 [n_pages][kv_heads][64][head_dim]
+ *   v        int8 [n_pages][kv_heads][head_dim][64]   (transposed in the page)
+ *   k_scale  bf16 [n_pages][kv_heads][64];  v_scale likewise
+ *   table    int32 [batch][table_width]: the page of tokens 64 w .. 64 w + 63
+ *            of each sequence; entries past a sequence's length are not read
+ * kv_heads 1..1024; head_dim 64, 128 or 256; batch 1..4096; n_pages and
+ * table_width >= 1, table_width <= 2^18.  Host struct of device pointers.
+ *
+ * Indices live on the device, so the kernels check them: a page id outside
+ * the pool, a position outside the table, a row outside the call's rows or a
+ * length outside [0, ctx] sets bit 4 of the device error word
+ * (dvssq_device_error); the row is then skipped, the page's keys are left out
+ * of the attention, the length is clamped, and nothing out of range is read
+ * or written.  Two rows of one call that land on the same slot (sequences
+ * that share a page) leave that slot undefined.                             */
+#define DVSSQ_KV_PAGE 64
+typedef struct {
+  int8_t *k;
+  int8_t *v;
+  uint16_t *k_scale;
+  uint16_t *v_scale;
+  const int32_t *table;
+  int32_t n_pages;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t batch;
+  int32_t table_width;
+} dvssq_kv_cache;
+
+/* Quantises K and V rows into the cache.  Row t of the call belongs to the
+ * sequence b with cu[b] <= t < cu[b+1], at position start[b] + t - cu[b];
+ * rows at and past cu[batch] (a padded call) are ignored.
+ *   k, v    bf16 (device): row t of head h starts at element
+ *           t * token_stride + h * head_stride and is contiguous; strides are
+ *           multiples of 8 elements and >= 0, so slices of a fused
+ *           projection's output are taken as they are
+ *   tokens  rows of k and v, 0 (a no-op) .. 2^30
+ *   start   int32 [batch] (device)
+ *   cu      int32 [batch + 1] (device), ascending from 0, or NULL: one row
+ *           per sequence (tokens == batch), the decode step's form
+ * Only the slots of the given rows are written.  Deterministic.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, DEVICE, CUDA.         */
+DVSSQ_API dvssq_status dvssq_kv_append(const dvssq_kv_cache *cache, const void *k,
+                                       int64_t k_token_stride, int64_t k_head_stride,
+                                       const void *v, int64_t v_token_stride,
+                                       int64_t v_head_stride, int64_t tokens,
+                                       const int32_t *start, const int32_t *cu, void *stream);
+
+/* Reads rows back: k_out, v_out bf16 [tokens][kv_heads][head_dim] (device),
+ * value RN_bf16(c s); rows, start and cu as in dvssq_kv_append (output rows at
+ * and past cu[batch], and skipped rows, are left as they were).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, DEVICE, CUDA.         */
+DVSSQ_API dvssq_status dvssq_kv_read(const dvssq_kv_cache *cache, void *k_out, void *v_out,
+                                     int64_t tokens, const int32_t *start, const int32_t *cu,
+                                     void *stream);
+
+/* Bytes of workspace dvssq_bss_attention_q8 needs (host only).  Of `shape`,
+ * ctx is an upper bound on the lengths (0 <= lens[b] <= ctx).  Limits: batch
+ * 1..4096, q_heads a multiple of kv_heads with at most 16 query heads per KV
+ * head, kv_heads 1..1024, head_dim 64, 128 or 256, ctx 1..2^24.             */
+DVSSQ_API dvssq_status dvssq_bss_attention_q8_workspace_size(const dvssq_attn_shape *shape,
+                                                             size_t *bytes);
+
+/* KV-BSS decode attention (the equations of dvssq_bss_attention) of one query
+ * token per sequence over the 8-bit cache, each sequence over its own length.
+ *   shape   kv_heads, head_dim and batch as the cache's; ctx <= 64 *
+ *           table_width; tau and haze as in dvssq_bss_attention
+ *   q       bf16 (device): head h of sequence b starts at element
+ *           b * q_batch_stride + h * q_head_stride; strides multiples of 8
+ *   lens    int32 [batch] (device); a sequence of length 0 gets zeros
+ *   out     [batch][q_heads][head_dim] (device), fp32 or bf16 by y_dtype
+ *           (DVSSQ_Y_*; bf16 rounds the fp32 result to nearest even)
+ * Logits, maxima, weights and sums are FP32.  Results are deterministic.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, DEVICE, CUDA. */
+DVSSQ_API dvssq_status dvssq_bss_attention_q8(const dvssq_attn_shape *shape,
+                                              const dvssq_kv_cache *cache, const void *q,
+                                              int64_t q_batch_stride, int64_t q_head_stride,
+                                              const int32_t *lens, void *out, int32_t y_dtype,
+                                              void *workspace, size_t workspace_bytes,
+                                              void *stream);
+
+/* Bytes of workspace dvssq_bss_attention_prefix needs (host only);
+ * prefix_len 0..2^24, other limits as dvssq_bss_attention_q8_workspace_size. */
+DVSSQ_API dvssq_status dvssq_bss_attention_prefix_workspace_size(const dvssq_attn_shape *shape,
+                                                                 int32_t prefix_len,
+                                                                 size_t *bytes);
+
+/* dvssq_bss_attention_q8 for a batch whose sequences share a prefix: every
+ * sequence attends to the prefix_len keys of the pages prefix_table lists and
+ * then to its own lens[b] keys (the cache's table holds its own part only, from
+ * its own position 0; the prefix may end inside a page).  The prefix is read
+ * once for the whole batch.
+ *   prefix_table  int32 [ceil(prefix_len / 64)] (device; may be NULL when
+ *                 prefix_len is 0)
+ * A sequence with neither prefix nor own keys gets zeros.  Results are
+ * deterministic.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, DEVICE, CUDA. */
+DVSSQ_API dvssq_status dvssq_bss_attention_prefix(const dvssq_attn_shape *shape,
+                                                  const dvssq_kv_cache *cache,
+                                                  const int32_t *prefix_table,
+                                                  int32_t prefix_len, const void *q,
+                                                  int64_t q_batch_stride, int64_t q_head_stride,
+                                                  const int32_t *lens, void *out,
+                                                  int32_t y_dtype, void *workspace,
+                                                  size_t workspace_bytes, void *stream);
+
 /* Allocation-free decode forward.  The paper has no counterpart: this entry
  * exists for callers that cannot obtain device memory for a workspace --
  * for example a host program that links only this library and has no device
@@ -421,7 +536,8 @@ DVSSQ_API dvssq_status dvssq_mlp_stack_forward(const dvssq_mlp_layer *layers, in
 /* Reads (and clears when `clear` != 0) the device error word of the current
  * device; synchronises the device.  0 means no kernel gave up a wait; bit 0:
  * an mbarrier wait ran out, bit 1: a tensor-memory accumulator wait, bit 2:
- * a kernel saw an unsupported shape, bit 3: a grid-barrier wait.          */
+ * a kernel saw an unsupported shape, bit 3: a grid-barrier wait, bit 4: an
+ * index of a KV-cache call out of range.                                   */
 DVSSQ_API dvssq_status dvssq_device_error(uint32_t *word, int32_t clear);
 
 /* Wait limit of every bounded wait in the library's kernels, in SM clock

@@ -10,9 +10,11 @@ Functions keep the C names (see include/dvssq.h):
     dvssq_fwht, dvssq_encode_workspace_size, dvssq_encode,
     dvssq_forward_workspace_size, dvssq_linear_forward, dvssq_device_error,
     dvssq_mlp_stack_workspace_size, dvssq_mlp_stack_prepare,
-    dvssq_mlp_stack_forward, dvssq_profile_* .
+    dvssq_mlp_stack_forward, dvssq_kv_append, dvssq_kv_read,
+    dvssq_bss_attention_q8, dvssq_bss_attention_prefix, dvssq_profile_* .
 ``DvssqLinear`` bundles one encoded layer with its workspaces; ``MlpStack``
-bundles a stack of gated-GELU MLP blocks with its prepared workspace.
+bundles a stack of gated-GELU MLP blocks with its prepared workspace;
+``KvCache`` holds the tensors of an 8-bit paged KV cache.
 """
 from __future__ import annotations
 
@@ -28,6 +30,9 @@ __all__ = [
     "dvssq_forward_workspace_size", "dvssq_linear_forward", "dvssq_linear_forward_static",
     "dvssq_materialize", "dvssq_lowrank_workspace_size", "dvssq_lowrank", "AttnShape",
     "dvssq_bss_attention_workspace_size", "dvssq_bss_attention", "dvssq_device_error", "STATIC_SCRATCH_BYTES", "MlpStack",
+    "KvCache", "KV_PAGE", "dvssq_kv_append", "dvssq_kv_read",
+    "dvssq_bss_attention_q8_workspace_size", "dvssq_bss_attention_q8",
+    "dvssq_bss_attention_prefix_workspace_size", "dvssq_bss_attention_prefix",
     "dvssq_mlp_stack_workspace_size", "dvssq_mlp_stack_plan_query", "dvssq_mlp_stack_prepare",
     "dvssq_mlp_stack_forward", "dvssq_profile_enable", "dvssq_profile_collect", "dvssq_profile_read",
     "dvssq_profile_reset", "dvssq_set_wait_limit", "dvssq_selftest_wait",
@@ -54,7 +59,10 @@ EXPORTED_SYMBOLS = (
     "dvssq_encode_workspace_size", "dvssq_encode", "dvssq_forward_workspace_size",
     "dvssq_linear_forward", "dvssq_linear_forward_static", "dvssq_materialize",
     "dvssq_lowrank_workspace_size", "dvssq_lowrank", "dvssq_bss_attention_workspace_size",
-    "dvssq_bss_attention", "dvssq_device_error", "dvssq_mlp_stack_workspace_size",
+    "dvssq_bss_attention", "dvssq_kv_append", "dvssq_kv_read",
+    "dvssq_bss_attention_q8_workspace_size", "dvssq_bss_attention_q8",
+    "dvssq_bss_attention_prefix_workspace_size", "dvssq_bss_attention_prefix",
+    "dvssq_device_error", "dvssq_mlp_stack_workspace_size",
     "dvssq_mlp_stack_plan_query", "dvssq_mlp_stack_prepare", "dvssq_mlp_stack_forward",
     "dvssq_profile_enable",
     "dvssq_profile_collect", "dvssq_profile_count", "dvssq_profile_get",
@@ -98,6 +106,14 @@ class AttnShape(ctypes.Structure):
                 ("ctx", ctypes.c_int32), ("tau", ctypes.c_float), ("haze", ctypes.c_float)]
 
 
+class _KvCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("table_width", ctypes.c_int32)]
+
+
 class _EncodeInfo(ctypes.Structure):
     _fields_ = [("inexact_rotation_blocks", ctypes.c_int64),
                 ("fp16_unsafe_scales", ctypes.c_int64),
@@ -131,6 +147,22 @@ _sig = {
     "dvssq_lowrank": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                      ctypes.c_int32, ctypes.c_uint64, _P, _P, _P, _P,
                                      ctypes.c_size_t, _P]),
+    "dvssq_kv_append": (ctypes.c_int, [ctypes.POINTER(_KvCacheC), _P, ctypes.c_int64, ctypes.c_int64,
+                                       _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P,
+                                       _P]),
+    "dvssq_kv_read": (ctypes.c_int, [ctypes.POINTER(_KvCacheC), _P, _P, ctypes.c_int64, _P, _P, _P]),
+    "dvssq_bss_attention_q8_workspace_size": (ctypes.c_int, [ctypes.POINTER(AttnShape),
+                                                             ctypes.POINTER(ctypes.c_size_t)]),
+    "dvssq_bss_attention_q8": (ctypes.c_int, [ctypes.POINTER(AttnShape), ctypes.POINTER(_KvCacheC),
+                                              _P, ctypes.c_int64, ctypes.c_int64, _P, _P,
+                                              ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "dvssq_bss_attention_prefix_workspace_size": (ctypes.c_int, [ctypes.POINTER(AttnShape),
+                                                                 ctypes.c_int32,
+                                                                 ctypes.POINTER(ctypes.c_size_t)]),
+    "dvssq_bss_attention_prefix": (ctypes.c_int, [ctypes.POINTER(AttnShape),
+                                                  ctypes.POINTER(_KvCacheC), _P, ctypes.c_int32,
+                                                  _P, ctypes.c_int64, ctypes.c_int64, _P, _P,
+                                                  ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "dvssq_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]),
     "dvssq_mlp_stack_workspace_size": (ctypes.c_int, [ctypes.POINTER(_MlpLayer), ctypes.c_int32,
                                                       ctypes.POINTER(ctypes.c_size_t)]),
@@ -341,6 +373,230 @@ def dvssq_bss_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tau: 
                                    _ptr(workspace), workspace.numel(), _stream(stream)),
            "dvssq_bss_attention")
     return out
+
+
+KV_PAGE = 64
+
+
+def _launch(device, stream, body):
+    """body(stream handle) with ``device`` current; new tensors belong to ``stream``."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    with torch.cuda.device(device):
+        if stream is None:
+            return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        s = stream
+        if not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(stream), device=device)
+        if s.device != device:
+            raise ValueError(f"the stream belongs to {s.device}, the tensors to {device}")
+        with torch.cuda.stream(s):
+            return body(ctypes.c_void_p(s.cuda_stream))
+
+
+def _indices(t, name, n, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold {n} values, got shape {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t, name, shape, device):
+    """Pointer and (outer, head) strides of BF16 rows [n][heads][d] whose last axis is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    # the stride of an axis of length one is never used
+    return ctypes.c_void_p(t.data_ptr()), 0 if shape[0] == 1 else a, 0 if shape[1] == 1 else b
+
+
+def _result(t, name, shape, dtype, device):
+    """``t``, checked, or a new tensor: a call's contiguous result."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    return t
+
+
+class KvCache:
+    """An 8-bit paged KV cache (layouts of dvssq_kv_cache): the tensors of the
+    page pool and the page table of a batch of sequences.
+
+    ``k`` int8 [pages][kv_heads][64][d], ``v`` int8 [pages][kv_heads][d][64],
+    ``k_scale`` and ``v_scale`` bfloat16 [pages][kv_heads][64], ``table`` int32
+    [batch][width], all contiguous and on one CUDA device.  The caller owns the
+    assignment of pages; several KvCache objects may share a pool.
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "table", "device", "_c")
+
+    def __init__(self, k, v, k_scale, v_scale, table):
+        if k.dim() != 4 or table.dim() != 2:
+            raise ValueError("k must be [pages][kv_heads][64][d] and table [batch][width]")
+        P, H, page, d = k.shape
+        dev = k.device
+        want = ((k, "k", torch.int8, (P, H, KV_PAGE, d)), (v, "v", torch.int8, (P, H, d, KV_PAGE)),
+                (k_scale, "k_scale", torch.bfloat16, (P, H, KV_PAGE)),
+                (v_scale, "v_scale", torch.bfloat16, (P, H, KV_PAGE)),
+                (table, "table", torch.int32, tuple(table.shape)))
+        for t, name, dtype, shape in want:
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
+            if t.device != dev or not t.is_cuda:
+                raise ValueError(f"{name} is on {t.device}: the cache lives on one CUDA device")
+        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+        self.device = dev
+        self._c = _KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                            table.data_ptr(), P, H, d, table.shape[0], table.shape[1])
+
+    @classmethod
+    def zeros(cls, pages: int, kv_heads: int, head_dim: int, table: torch.Tensor):
+        """A cleared pool of ``pages`` pages on the table's device."""
+        z = lambda *s, dtype=torch.int8: torch.zeros(s, dtype=dtype, device=table.device)  # noqa: E731
+        return cls(z(pages, kv_heads, KV_PAGE, head_dim), z(pages, kv_heads, head_dim, KV_PAGE),
+                   z(pages, kv_heads, KV_PAGE, dtype=torch.bfloat16),
+                   z(pages, kv_heads, KV_PAGE, dtype=torch.bfloat16), table)
+
+
+def dvssq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor,
+                    cu: torch.Tensor | None = None, stream=None):
+    """Quantise BF16 rows k, v [T][kv_heads][d] into the cache's pages.
+
+    Row t of sequence b (cu[b] <= t < cu[b+1]; without ``cu``, t = b) goes to
+    position start[b] + t - cu[b].  k and v may be slices with any token and
+    head strides that are multiples of 8 elements.
+    """
+    c = cache._c
+    T = k.shape[0]
+    shape = (T, c.kv_heads, c.head_dim)
+    kp, kt, kh = _rows(k, "k", shape, cache.device)
+    vp, vt, vh = _rows(v, "v", shape, cache.device)
+    sp = _indices(start, "start", c.batch, cache.device)
+    cp = None if cu is None else _indices(cu, "cu", c.batch + 1, cache.device)
+    _launch(cache.device, stream, lambda st: _check(
+        lib.dvssq_kv_append(ctypes.byref(c), kp, kt, kh, vp, vt, vh, T, sp, cp, st),
+        "dvssq_kv_append"))
+
+
+def dvssq_kv_read(cache: KvCache, start: torch.Tensor, cu: torch.Tensor | None = None,
+                  tokens: int | None = None, k: torch.Tensor | None = None,
+                  v: torch.Tensor | None = None, stream=None):
+    """Rows read back as BF16: (k, v), each [tokens][kv_heads][d].
+
+    Rows, ``start`` and ``cu`` as in dvssq_kv_append; ``tokens`` (cu's last
+    value, known to the caller) may be left out without ``cu``.  Rows that the
+    call does not cover are left as they were (new tensors: undefined).
+    """
+    c = cache._c
+    if tokens is None:
+        if cu is not None:
+            raise ValueError("tokens is needed with cu: its last value lives on the device")
+        tokens = c.batch
+    shape = (int(tokens), c.kv_heads, c.head_dim)
+    sp = _indices(start, "start", c.batch, cache.device)
+    cp = None if cu is None else _indices(cu, "cu", c.batch + 1, cache.device)
+
+    def body(st):
+        ko = _result(k, "k", shape, torch.bfloat16, cache.device)
+        vo = _result(v, "v", shape, torch.bfloat16, cache.device)
+        _check(lib.dvssq_kv_read(ctypes.byref(c), ko.data_ptr(), vo.data_ptr(), shape[0], sp, cp, st),
+               "dvssq_kv_read")
+        return ko, vo
+
+    return _launch(cache.device, stream, body)
+
+
+def dvssq_bss_attention_q8_workspace_size(shape: AttnShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.dvssq_bss_attention_q8_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "dvssq_bss_attention_q8_workspace_size")
+    return n.value
+
+
+def dvssq_bss_attention_prefix_workspace_size(shape: AttnShape, prefix_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.dvssq_bss_attention_prefix_workspace_size(ctypes.byref(shape), int(prefix_len),
+                                                         ctypes.byref(n)),
+           "dvssq_bss_attention_prefix_workspace_size")
+    return n.value
+
+
+def _attention_q8(where, q, cache, lens, prefix, prefix_len, tau, haze, ctx, out, y_dtype,
+                  workspace, stream):
+    c, dev = cache._c, cache.device
+    if q.dim() != 3:
+        raise ValueError("q must be [batch][q_heads][head_dim]")
+    Hq = q.shape[1]
+    qp, qb, qh = _rows(q, "q", (c.batch, Hq, c.head_dim), dev)
+    lp = _indices(lens, "lens", c.batch, dev)
+    if y_dtype not in (Y_F32, Y_BF16):
+        raise ValueError("y_dtype must be Y_F32 or Y_BF16")
+    dtype = torch.float32 if y_dtype == Y_F32 else torch.bfloat16
+    shape = AttnShape(c.batch, Hq, c.kv_heads, c.head_dim,
+                      KV_PAGE * c.table_width if ctx is None else int(ctx), tau, haze)
+    if prefix is None:
+        need = dvssq_bss_attention_q8_workspace_size(shape)
+    else:
+        need = dvssq_bss_attention_prefix_workspace_size(shape, prefix_len)
+
+    def body(st):
+        o = _result(out, "out", (c.batch, Hq, c.head_dim), dtype, dev)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        nb = ws.numel() * ws.element_size()
+        if prefix is None:
+            s = lib.dvssq_bss_attention_q8(ctypes.byref(shape), ctypes.byref(c), qp, qb, qh, lp,
+                                           o.data_ptr(), y_dtype, ws.data_ptr(), nb, st)
+        else:
+            s = lib.dvssq_bss_attention_prefix(ctypes.byref(shape), ctypes.byref(c), prefix,
+                                               prefix_len, qp, qb, qh, lp, o.data_ptr(), y_dtype,
+                                               ws.data_ptr(), nb, st)
+        _check(s, where)
+        return o
+
+    return _launch(dev, stream, body)
+
+
+def dvssq_bss_attention_q8(q: torch.Tensor, cache: KvCache, lens: torch.Tensor, tau: float = 1.10,
+                           haze: float = 12.0, ctx: int | None = None,
+                           out: torch.Tensor | None = None, y_dtype: int = Y_F32,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """KV-BSS decode attention over the 8-bit cache: q [B][Hq][d] (BF16) -> [B][Hq][d].
+
+    ``lens`` int32 [B]: each sequence's keys; ``ctx``: an upper bound on them
+    (the table's capacity when left out), which sizes the workspace.
+    """
+    return _attention_q8("dvssq_bss_attention_q8", q, cache, lens, None, 0, tau, haze, ctx, out,
+                         y_dtype, workspace, stream)
+
+
+def dvssq_bss_attention_prefix(q: torch.Tensor, cache: KvCache, lens: torch.Tensor,
+                               prefix_table: torch.Tensor, prefix_len: int, tau: float = 1.10,
+                               haze: float = 12.0, ctx: int | None = None,
+                               out: torch.Tensor | None = None, y_dtype: int = Y_F32,
+                               workspace: torch.Tensor | None = None, stream=None):
+    """dvssq_bss_attention_q8 for sequences that share a prefix of ``prefix_len``
+    keys in the pages of ``prefix_table`` (int32 [ceil(prefix_len / 64)]); the
+    cache's table and ``lens`` describe each sequence's own keys after it."""
+    n = int(prefix_len)
+    pp = _indices(prefix_table, "prefix_table", -(-n // KV_PAGE), cache.device)
+    return _attention_q8("dvssq_bss_attention_prefix", q, cache, lens, pp, n, tau, haze, ctx, out,
+                         y_dtype, workspace, stream)
 
 
 def dvssq_lowrank_workspace_size(M: int, K: int, rank: int) -> int:

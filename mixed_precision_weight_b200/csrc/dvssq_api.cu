@@ -399,6 +399,163 @@ dvssq_status dvssq_bss_attention(const dvssq_attn_shape *shape, const void *q, c
   return e == cudaSuccess ? DVSSQ_OK : cuda_fail(e);
 }
 
+// -------------------------------------------------------- 8-bit KV cache ---
+namespace {
+dvssq_status kv_pool(const dvssq_kv_cache *c, KvPool &p) {
+  if (c == nullptr) return DVSSQ_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return DVSSQ_ERR_UNSUPPORTED_SHAPE;
+  if (c->kv_heads < 1 || c->kv_heads > 1024 || c->batch < 1 || c->batch > 4096 ||
+      c->n_pages < 1 || c->table_width < 1 || c->table_width > (1 << 18))
+    return DVSSQ_ERR_UNSUPPORTED_SHAPE;
+  if (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
+      c->table == nullptr)
+    return DVSSQ_ERR_INVALID_ARG;
+  const void *bufs[] = {c->k, c->v, c->k_scale, c->v_scale, c->table};
+  for (const void *b : bufs)
+    if (!aligned16(b)) return DVSSQ_ERR_MISALIGNED;
+  p.k = c->k; p.v = c->v; p.ks = c->k_scale; p.vs = c->v_scale; p.table = c->table;
+  p.n_pages = c->n_pages; p.H = c->kv_heads; p.D = c->head_dim; p.B = c->batch;
+  p.W = c->table_width;
+  return DVSSQ_OK;
+}
+
+// Strides of a strided BF16 operand: its rows travel as 16-byte vectors.
+dvssq_status kv_strides(int64_t a, int64_t b) {
+  if (a < 0 || b < 0) return DVSSQ_ERR_INVALID_ARG;
+  if (a % 8 != 0 || b % 8 != 0) return DVSSQ_ERR_MISALIGNED;
+  return DVSSQ_OK;
+}
+
+dvssq_status kv_rows(const dvssq_kv_cache *c, int64_t tokens, const int32_t *start,
+                     const int32_t *cu, KvPool &p) {
+  const dvssq_status s = kv_pool(c, p);
+  if (s != DVSSQ_OK) return s;
+  if (tokens < 0 || tokens > ((int64_t)1 << 30)) return DVSSQ_ERR_INVALID_ARG;
+  if (tokens == 0) return DVSSQ_OK;
+  if (start == nullptr || (cu == nullptr && tokens != c->batch)) return DVSSQ_ERR_INVALID_ARG;
+  if (!aligned16(start) || !aligned16(cu)) return DVSSQ_ERR_MISALIGNED;
+  return DVSSQ_OK;
+}
+
+dvssq_status q8_shape(const dvssq_attn_shape *s, int32_t prefix_len, Q8Shape &o) {
+  if (s == nullptr) return DVSSQ_ERR_INVALID_ARG;
+  if (s->batch < 1 || s->batch > 4096 || s->kv_heads < 1 || s->kv_heads > 1024 ||
+      s->q_heads < 1 || s->q_heads % s->kv_heads != 0 || s->q_heads / s->kv_heads > 16)
+    return DVSSQ_ERR_UNSUPPORTED_SHAPE;
+  if (s->head_dim != 64 && s->head_dim != 128 && s->head_dim != 256)
+    return DVSSQ_ERR_UNSUPPORTED_SHAPE;
+  if (s->ctx < 1 || s->ctx > (1 << 24) || prefix_len > (1 << 24)) return DVSSQ_ERR_UNSUPPORTED_SHAPE;
+  if (prefix_len < 0) return DVSSQ_ERR_INVALID_ARG;
+  if (!(s->tau > 0.f) || s->tau > 1e30f || s->haze != s->haze) return DVSSQ_ERR_INVALID_ARG;
+  o.B = s->batch; o.Hq = s->q_heads; o.Hkv = s->kv_heads; o.D = s->head_dim; o.ctx = s->ctx;
+  o.prefix = prefix_len;
+  return DVSSQ_OK;
+}
+
+dvssq_status q8_size(const dvssq_attn_shape *shape, int32_t prefix_len, size_t *bytes) {
+  if (bytes == nullptr) return DVSSQ_ERR_INVALID_ARG;
+  Q8Shape qs{};
+  const dvssq_status s = q8_shape(shape, prefix_len, qs);
+  if (s != DVSSQ_OK) return s;
+  *bytes = q8_workspace_bytes(qs);
+  return DVSSQ_OK;
+}
+
+dvssq_status q8_attention(const dvssq_attn_shape *shape, const dvssq_kv_cache *cache,
+                          const int32_t *prefix_table, int32_t prefix_len, const void *q,
+                          int64_t q_bs, int64_t q_hs, const int32_t *lens, void *out,
+                          int32_t y_dtype, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+  Q8Args a{};
+  dvssq_status s = q8_shape(shape, prefix_len, a.s);
+  if (s != DVSSQ_OK) return s;
+  if ((s = kv_pool(cache, a.pool)) != DVSSQ_OK) return s;
+  if (cache->batch != shape->batch || cache->kv_heads != shape->kv_heads ||
+      cache->head_dim != shape->head_dim || shape->ctx > 64LL * cache->table_width)
+    return DVSSQ_ERR_INVALID_ARG;
+  if (q == nullptr || lens == nullptr || out == nullptr || workspace == nullptr ||
+      (prefix_len > 0 && prefix_table == nullptr))
+    return DVSSQ_ERR_INVALID_ARG;
+  if (y_dtype != DVSSQ_Y_F32 && y_dtype != DVSSQ_Y_BF16) return DVSSQ_ERR_INVALID_ARG;
+  if ((s = kv_strides(q_bs, q_hs)) != DVSSQ_OK) return s;
+  const void *bufs[] = {q, lens, out, prefix_len > 0 ? prefix_table : nullptr};
+  for (const void *b : bufs)
+    if (!aligned16(b)) return DVSSQ_ERR_MISALIGNED;
+  if (!aligned256(workspace)) return DVSSQ_ERR_MISALIGNED;
+  if (workspace_bytes < q8_workspace_bytes(a.s)) return DVSSQ_ERR_WORKSPACE;
+  if ((s = ensure_device()) != DVSSQ_OK) return s;
+  a.q = static_cast<const uint16_t *>(q);
+  a.q_bs = q_bs; a.q_hs = q_hs;
+  a.lens = lens; a.ptable = prefix_table;
+  a.tau = shape->tau; a.haze = shape->haze;
+  a.out = out; a.out_bf16 = y_dtype == DVSSQ_Y_BF16;
+  a.workspace = workspace;
+  const cudaError_t e = launch_q8_attention(a, static_cast<cudaStream_t>(stream), launcher());
+  return e == cudaSuccess ? DVSSQ_OK : cuda_fail(e);
+}
+}  // namespace
+
+dvssq_status dvssq_kv_append(const dvssq_kv_cache *cache, const void *k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                             int64_t v_head_stride, int64_t tokens, const int32_t *start,
+                             const int32_t *cu, void *stream) {
+  KvPool pool{};
+  dvssq_status s = kv_rows(cache, tokens, start, cu, pool);
+  if (s != DVSSQ_OK || tokens == 0) return s;
+  if (k == nullptr || v == nullptr) return DVSSQ_ERR_INVALID_ARG;
+  if ((s = kv_strides(k_token_stride, k_head_stride)) != DVSSQ_OK) return s;
+  if ((s = kv_strides(v_token_stride, v_head_stride)) != DVSSQ_OK) return s;
+  if (!aligned16(k) || !aligned16(v)) return DVSSQ_ERR_MISALIGNED;
+  if ((s = ensure_device()) != DVSSQ_OK) return s;
+  const long long strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  const cudaError_t e = launch_kv_append(pool, static_cast<const uint16_t *>(k),
+                                         static_cast<const uint16_t *>(v), strides, tokens, start,
+                                         cu, static_cast<cudaStream_t>(stream), launcher());
+  return e == cudaSuccess ? DVSSQ_OK : cuda_fail(e);
+}
+
+dvssq_status dvssq_kv_read(const dvssq_kv_cache *cache, void *k_out, void *v_out, int64_t tokens,
+                           const int32_t *start, const int32_t *cu, void *stream) {
+  KvPool pool{};
+  dvssq_status s = kv_rows(cache, tokens, start, cu, pool);
+  if (s != DVSSQ_OK || tokens == 0) return s;
+  if (k_out == nullptr || v_out == nullptr) return DVSSQ_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return DVSSQ_ERR_MISALIGNED;
+  if ((s = ensure_device()) != DVSSQ_OK) return s;
+  const cudaError_t e = launch_kv_read(pool, static_cast<uint16_t *>(k_out),
+                                       static_cast<uint16_t *>(v_out), tokens, start, cu,
+                                       static_cast<cudaStream_t>(stream), launcher());
+  return e == cudaSuccess ? DVSSQ_OK : cuda_fail(e);
+}
+
+dvssq_status dvssq_bss_attention_q8_workspace_size(const dvssq_attn_shape *shape, size_t *bytes) {
+  return q8_size(shape, 0, bytes);
+}
+
+dvssq_status dvssq_bss_attention_q8(const dvssq_attn_shape *shape, const dvssq_kv_cache *cache,
+                                    const void *q, int64_t q_batch_stride, int64_t q_head_stride,
+                                    const int32_t *lens, void *out, int32_t y_dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+  return q8_attention(shape, cache, nullptr, 0, q, q_batch_stride, q_head_stride, lens, out,
+                      y_dtype, workspace, workspace_bytes, stream);
+}
+
+dvssq_status dvssq_bss_attention_prefix_workspace_size(const dvssq_attn_shape *shape,
+                                                       int32_t prefix_len, size_t *bytes) {
+  return q8_size(shape, prefix_len, bytes);
+}
+
+dvssq_status dvssq_bss_attention_prefix(const dvssq_attn_shape *shape, const dvssq_kv_cache *cache,
+                                        const int32_t *prefix_table, int32_t prefix_len,
+                                        const void *q, int64_t q_batch_stride,
+                                        int64_t q_head_stride, const int32_t *lens, void *out,
+                                        int32_t y_dtype, void *workspace, size_t workspace_bytes,
+                                        void *stream) {
+  return q8_attention(shape, cache, prefix_table, prefix_len, q, q_batch_stride, q_head_stride,
+                      lens, out, y_dtype, workspace, workspace_bytes, stream);
+}
+
 // ------------------------------------------------------------- MLP stack ---
 namespace {
 // Host-side checks of a stack and its flattening into matrix descriptors.

@@ -226,6 +226,38 @@ struct BssArgs {
 size_t bss_workspace_bytes(int B, int Hq, int L, int D);
 cudaError_t launch_bss_attention(const BssArgs &a, cudaStream_t st, Launcher &L);
 
+// ------------------------------------------------------------ 8-bit KV cache -
+// The pool of pages and the sequences' page table (device pointers).
+struct KvPool {
+  int8_t *k, *v;
+  uint16_t *ks, *vs;
+  const int32_t *table;        // [B][W]
+  int n_pages, H, D, B, W;
+};
+// strides: K token, K head, V token, V head, in elements
+cudaError_t launch_kv_append(const KvPool &c, const uint16_t *k, const uint16_t *v,
+                             const long long *strides, long long T, const int32_t *start,
+                             const int32_t *cu, cudaStream_t st, Launcher &L);
+cudaError_t launch_kv_read(const KvPool &c, uint16_t *k, uint16_t *v, long long T,
+                           const int32_t *start, const int32_t *cu, cudaStream_t st, Launcher &L);
+
+struct Q8Shape {
+  int B, Hq, Hkv, D, ctx, prefix;
+};
+struct Q8Args {
+  Q8Shape s;
+  KvPool pool;
+  const uint16_t *q;
+  long long q_bs, q_hs;        // sequence and head strides in elements
+  const int32_t *lens, *ptable;
+  float tau, haze;
+  void *out;
+  int out_bf16;
+  void *workspace;
+};
+size_t q8_workspace_bytes(const Q8Shape &s);
+cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L);
+
 // Tensor-map encoder from the driver (resolved once through the runtime).
 CUresult encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
                         uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
