@@ -1,28 +1,58 @@
 // KV-BSS decode attention over the 8-bit paged cache (Spark card, "2. KV-BSS:
 // Key-Value Binding Softmax Sharpening"), for one query token per sequence
-// with grouped-query heads, over an optional prefix that all sequences share
-// and each sequence's own keys:
+// with grouped-query heads (G query heads share a KV head):
 //   s_l = (q . k_l) tau / sqrt(d),  m = max_l s_l,
 //   p_l = exp(s_l - m) if s_l >= m - haze else 0,  out = sum_l p_l v_l / sum_l p_l
 // with k_l = ks_l kc_l and v_l = vs_l vc_l.  The haze threshold needs the final
-// maximum before any weight is known, so the logits are formed in a first pass.
-//   q8_logits  one CTA per (page, KV head, sequence): a warp per key
-//   q8_out     one CTA per (query head, sequence): maximum, weights, sum p v
+// maximum before any weight is known, so the context is walked twice, K then V,
+// each byte read once (HBM-bound: 2 (d + 2) bytes per key and KV head):
+//   q8_logits  logits of the keys, FP32, and each item's maximum per head
+//   q8_pv      weights from the final maximum, and each item's sum of p v; the V
+//              codes of a page whose 64 keys all fell below the threshold are
+//              never read
+//   q8_merge   the items' partials added in order, divided, stored
+// An item is a run of pages of one sequence and one KV head.  The lengths live
+// on the device, so every CTA derives the same plan from them: pages per item
+// such that the items fill whole rounds of the grid.
+//
+// Both contractions run on mma.sync straight from global memory: the page
+// layout puts the contracted axis in the innermost position, the order along
+// a contracted axis is free, so lane (g, tig) of a fragment takes 16 contiguous
+// bytes per row and no shared-memory staging or transposition is needed.
+//   q . k   m16n8k32 s8: 16 keys x 32 dimensions against 4 heads x 2 limbs.
+//           The query is a 16-bit integer of a power-of-two step, 256 hi + lo
+//           with both limbs in s8, so the integer sums are exact.
+//   p v     m16n8k16 bf16: 16 dimensions x 16 keys against 4 heads x 2 limbs.
+//           A code is exact in BF16; a weight p vs is split into two BF16 limbs
+//           (2^-17 relative, any magnitude), so the sums are FP32-grade.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace dvssq {
+
+constexpr int kQ8Threads = 128;
+constexpr int kQ8MaxPages = 16;        // pages per item at most
+constexpr int kQ8Sms = 148;            // B200; any value gives the same results
+
+// n-tiles of 4 heads x 2 limbs that cover G heads
+__host__ __device__ constexpr int q8_tiles(int G) { return G <= 4 ? 1 : G <= 8 ? 2 : 4; }
+// resident CTAs per SM the kernels are compiled for (registers: query fragments
+// and accumulators grow with the tiles)
+__host__ __device__ constexpr int q8_occ(int NT) { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
 
 struct Q8Params {
   const uint16_t *q;
   long long q_bs, q_hs;
   const int8_t *k, *v;
   const uint16_t *ks, *vs;
-  const int32_t *table, *ptable, *lens;
+  const int32_t *table, *lens;
   void *out;
   int out_bf16;
-  float *logit;                  // [B][Hq][PL + ctx]
-  int B, Hq, H, G, W, n_pages, ctx, prefix, ppages;
+  float *logit;                  // [B][H][ctxp][4 NT]
+  float *cmax, *psum;            // [items][4 NT]
+  float *pacc;                   // [items][G][D]
+  int *off;                      // [B + 1] first item of each sequence (per KV head)
+  int B, Hq, H, G, W, n_pages, ctx, ctxp, target;
   float scale, haze;
 };
 
@@ -32,100 +62,566 @@ __device__ __forceinline__ int q8_len(const Q8Params &p, int b) {
   return max(0, min(n, p.ctx));
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) q8_logits_kernel(const Q8Params p) {
-  constexpr int VPL = D / 32;
-  const int w = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool pre = w < p.ppages;
-  const int own = w - p.ppages, keys = pre ? p.prefix - 64 * w : q8_len(p, b) - 64 * own;
-  if (keys <= 0) return;
-  const int page = pre ? p.ptable[w] : p.table[(size_t)b * p.W + own];
-  const bool ok = page >= 0 && page < p.n_pages;
-  if (!ok) set_error(kErrBadIndex);
-  const size_t ph = (size_t)(ok ? page : 0) * p.H + h;
-  for (int i = warp; i < min(keys, 64); i += 4) {
-    const float ks = bf16_bits_to_f32(p.ks[ph * 64 + i]);
-    float kf[VPL];
-    for (int u = 0; u < VPL; ++u) kf[u] = (float)p.k[(ph * 64 + i) * D + lane * VPL + u];
-    for (int g = 0; g < p.G; ++g) {
-      const uint16_t *q = p.q + b * p.q_bs + (h * p.G + g) * p.q_hs + lane * VPL;
-      float s = 0.f;
-      for (int u = 0; u < VPL; ++u) s = fmaf(bf16_bits_to_f32(q[u]), kf[u], s);
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0)
-        p.logit[((size_t)b * p.Hq + h * p.G + g) * (64 * p.ppages + p.ctx) + 64 * w + i] =
-            ok ? s * ks * p.scale : -INFINITY;
-    }
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(D) q8_out_kernel(const Q8Params p) {
-  __shared__ float red[32], wt[64];
-  const int hq = blockIdx.x, b = blockIdx.y, h = hq / p.G, tid = threadIdx.x;
-  const int len = q8_len(p, b), n = 64 * p.ppages + len;
-  const float *lg = p.logit + ((size_t)b * p.Hq + hq) * (64 * p.ppages + p.ctx);
-  auto live = [&](int i) { return i < p.prefix || i >= 64 * p.ppages; };
-  float m = -INFINITY;
-  for (int i = tid; i < n; i += D)
-    if (live(i)) m = fmaxf(m, lg[i]);
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) red[tid >> 5] = m;
+// The plan, the same in every CTA: off[b] = items of the sequences before b (per KV
+// head) in shared memory; returns the pages per item.  N page-heads over r
+// rounds of `target` CTAs, r the fewest whose items stay within kQ8MaxPages.
+__device__ __forceinline__ int q8_plan(const Q8Params &p, int *off) {
+  __shared__ int part[kQ8Threads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (p.B + kQ8Threads - 1) / kQ8Threads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += (q8_len(p, b) + 63) >> 6;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) part[warp] = sum;
   __syncthreads();
-  m = -INFINITY;
-  for (int i = 0; i < D / 32; ++i) m = fmaxf(m, red[i]);
-  float acc = 0.f, sum = 0.f;
-  for (int w = 0; 64 * w < n; ++w) {
-    const bool pre = w < p.ppages;
-    const int page = pre ? p.ptable[w] : p.table[(size_t)b * p.W + w - p.ppages];
-    if (page < 0 || page >= p.n_pages) continue;
-    const size_t ph = (size_t)page * p.H + h;
-    __syncthreads();
-    if (tid < 64) {
-      const int i = 64 * w + tid;
-      const float s = i < n && live(i) ? lg[i] : -INFINITY;
-      wt[tid] = s == -INFINITY || (p.haze > 0.f && s < m - p.haze) ? 0.f : expf(s - m);
-    }
-    __syncthreads();
-    for (int i = 0; i < 64; ++i)
-      if (wt[i] != 0.f) {
-        sum += wt[i];
-        acc = fmaf(wt[i] * bf16_bits_to_f32(p.vs[ph * 64 + i]), (float)p.v[(ph * D + tid) * 64 + i], acc);
-      }
+  long long N = 0;
+#pragma unroll
+  for (int i = 0; i < kQ8Threads / 32; ++i) N += part[i];
+  N *= p.H;
+  const long long round = (long long)p.target * kQ8MaxPages;
+  const long long r = max(1LL, (N + round - 1) / round);
+  const int c = (int)max(1LL, (N + p.target * r - 1) / (p.target * r));
+  int items = 0;
+  for (int b = b0; b < b1; ++b) items += (((q8_len(p, b) + 63) >> 6) + c - 1) / c;
+  int scan = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += t;
   }
-  const float o = sum == 0.f ? 0.f : acc / sum;
-  const size_t at = ((size_t)b * p.Hq + hq) * D + tid;
-  if (p.out_bf16) static_cast<uint16_t *>(p.out)[at] = f32_to_bf16_rn_bits(o);
-  else static_cast<float *>(p.out)[at] = o;
+  __syncthreads();
+  if (lane == 31) part[warp] = scan;
+  __syncthreads();
+  int base = scan - items;
+  for (int i = 0; i < warp; ++i) base += part[i];
+  for (int b = b0; b < b1; ++b) {
+    off[b] = base;
+    base += (((q8_len(p, b) + 63) >> 6) + c - 1) / c;
+  }
+  if (b1 == p.B && b0 < b1) off[p.B] = base;
+  __syncthreads();
+  return c;
 }
 
-size_t q8_workspace_bytes(const Q8Shape &s) {
-  return (size_t)s.B * s.Hq * (((s.prefix + 63) & ~63) + (size_t)s.ctx) * 4 + 256;
+// Sequence of item u (the last b with off[b] <= u and items of its own)
+__device__ __forceinline__ int q8_find(const int *off, int B, int u) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// D(16x8, s32) += A(16x32, s8, row) * B(32x8, s8, col)
+__device__ __forceinline__ void mma_s8(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                       uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D(16x8, f32) += A(16x16, bf16, row) * B(16x8, bf16, col)
+__device__ __forceinline__ void mma_bf16(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 q8_ldg(const int8_t *p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t word(const uint4 &u, int i) {
+  return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+}
+
+// Bytes 0, 2 (even) or 1, 3 (odd, x already shifted right by 8) of x as a BF16
+// pair: 128 + (low 7 bits), minus 128 or, with the sign bit, 256; all exact.
+__device__ __forceinline__ uint32_t q8_bf16_pair(uint32_t x) {
+  const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, c = (x & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+// One query head as limbs: 16-bit integers of step 2^(e - 14), e the exponent of
+// the head's largest magnitude (exact for BF16 values of the top 8 binades,
+// off by at most one unit below); hi and lo rows of bytes.  A whole warp.
+template <int D>
+__device__ __forceinline__ void q8_limbs(const uint16_t *q, int8_t *hi, int8_t *lo, float *step) {
+  constexpr int VPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  uint32_t bits[VPL], m = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    bits[i] = q[lane * VPL + i];
+    m = max(m, bits[i] & 0x7FFFu);
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  const int e = max((int)(m >> 7) - 127, -126);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    // the clamp only meets the mantissa 255/128, one unit above hi = lo = 127
+    const int x = m >= 0x7F80u ? 0 : min(__float2int_rn(ldexpf(bf16_bits_to_f32(bits[i]), 14 - e)), 32639);
+    const int l = ((x + 128) & 255) - 128;
+    lo[lane * VPL + i] = (int8_t)l;
+    hi[lane * VPL + i] = (int8_t)((x - l) >> 8);
+  }
+  if (lane == 0) *step = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, e - 14);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const Q8Params p) {
+  constexpr int DB = D / 64;                 // 64-byte blocks of a K row
+  constexpr int DEPTH = 8 / DB;              // pages in flight per warp
+  constexpr int GP = 4 * NT;
+  extern __shared__ int off[];
+  __shared__ __align__(16) int8_t limbs[8 * NT][D + 16];
+  __shared__ float s_step[GP];
+  __shared__ float s_max[kQ8Threads / 32][GP];
+  __shared__ int s_page[kQ8MaxPages];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  pdl_launch_dependents();
+  const int c = q8_plan(p, off);
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= p.B; b += kQ8Threads) p.off[b] = off[b];
+  const long long total = (long long)off[p.B] * p.H;
+  int held = -1;                             // the (sequence, KV head) whose limbs are held
+  uint32_t qf[NT][DB][4];
+  float step[NT];
+  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
+    const int u = (int)(item / p.H), h = (int)(item - (long long)u * p.H);
+    const int b = q8_find(off, p.B, u), len = q8_len(p, b);
+    const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
+    __syncthreads();                         // the previous item's shared memory is free
+    if (tid < np) {
+      int page = p.table[(size_t)b * p.W + p0 + tid];
+      if (page < 0 || page >= p.n_pages) {
+        set_error(kErrBadIndex);
+        page = -1;
+      }
+      s_page[tid] = page;
+    }
+    const bool fresh = held != b * p.H + h;
+    if (fresh) {
+      for (int i = warp; i < GP; i += kQ8Threads / 32) {
+        int8_t *hi = limbs[2 * i], *lo = limbs[2 * i + 1];
+        if (i < p.G) {
+          q8_limbs<D>(p.q + b * p.q_bs + (long long)(h * p.G + i) * p.q_hs, hi, lo, &s_step[i]);
+        } else {
+          for (int j = lane; j < D; j += 32) hi[j] = lo[j] = 0;
+          if (lane == 0) s_step[i] = 0.f;
+        }
+      }
+      held = b * p.H + h;
+    }
+    __syncthreads();
+    if (fresh) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < DB; ++j) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(&limbs[8 * nt + g][64 * j + 16 * tig]);
+          qf[nt][j][0] = w.x; qf[nt][j][1] = w.y; qf[nt][j][2] = w.z; qf[nt][j][3] = w.w;
+        }
+        step[nt] = s_step[4 * nt + tig] * p.scale;
+      }
+    }
+    // warp w: keys 16 w .. 16 w + 15 of every page; DEPTH pages' rows in flight
+    const int key = 16 * warp + g;
+    uint4 buf[DEPTH][DB][2];
+    uint16_t sc[DEPTH][2];
+    auto issue = [&](int pp, uint4 (*dst)[2], uint16_t *s) {
+      const size_t ph = (size_t)max(0, s_page[pp]) * p.H + h;
+      const int8_t *src = p.k + (ph * 64 + key) * D + 16 * tig;
+#pragma unroll
+      for (int j = 0; j < DB; ++j) {
+        dst[j][0] = q8_ldg(src + 64 * j);
+        dst[j][1] = q8_ldg(src + 8 * D + 64 * j);
+      }
+      s[0] = __ldg(p.ks + ph * 64 + key);
+      s[1] = __ldg(p.ks + ph * 64 + key + 8);
+    };
+    float mx[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mx[nt] = -INFINITY;
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (d < np) issue(d, buf[d], sc[d]);
+    float *lg = p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0) * GP;
+    for (int pb = 0; pb < np; pb += DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        const int pp = pb + d;
+        if (pp >= np) break;
+        int acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[nt][i] = 0;
+#pragma unroll
+        for (int j = 0; j < DB; ++j)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_s8(acc[nt], word(buf[d][j][0], 2 * s), word(buf[d][j][1], 2 * s),
+                     word(buf[d][j][0], 2 * s + 1), word(buf[d][j][1], 2 * s + 1), qf[nt][j][2 * s],
+                     qf[nt][j][2 * s + 1]);
+        const float k0 = bf16_bits_to_f32(sc[d][0]), k1 = bf16_bits_to_f32(sc[d][1]);
+        const bool ok = s_page[pp] >= 0;
+        if (pp + DEPTH < np) issue(pp + DEPTH, buf[d], sc[d]);
+        const int at = 64 * (p0 + pp) + key;
+        const bool v0 = ok && at < len, v1 = ok && at + 8 < len;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          // 256 hi + lo in exact integers, rounded once to FP32
+          const float l0 = v0 ? (float)(acc[nt][0] * 256 + acc[nt][1]) * k0 * step[nt] : -INFINITY;
+          const float l1 = v1 ? (float)(acc[nt][2] * 256 + acc[nt][3]) * k1 * step[nt] : -INFINITY;
+          lg[(64 * pp + key) * GP + 4 * nt + tig] = l0;
+          lg[(64 * pp + key + 8) * GP + 4 * nt + tig] = l1;
+          mx[nt] = fmaxf(mx[nt], fmaxf(l0, l1));
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], o));
+      if (lane < 4) s_max[warp][4 * nt + lane] = mx[nt];
+    }
+    __syncthreads();
+    if (tid < GP) {
+      float m = s_max[0][tid];
+#pragma unroll
+      for (int w = 1; w < kQ8Threads / 32; ++w) m = fmaxf(m, s_max[w][tid]);
+      p.cmax[item * GP + tid] = m;
+    }
+  }
+}
+
+// Weights of a page: [column][64 keys] of BF16, rows padded by 16 bytes so that a
+// fragment's loads (8 columns x 4 key groups) meet every bank once.  The keys
+// of each group of four are kept in the order 0, 2, 1, 3: a code word's even and
+// odd bytes are then the fragment's pairs.
+constexpr int kQ8WRow = 72;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8Params p) {
+  constexpr int MT = D / 64;                 // 16-row tiles of V^T per warp
+  constexpr int DEPTH = 8 / MT;              // pages in flight per warp
+  constexpr int GP = 4 * NT;
+  constexpr int NW = kQ8Threads / 32;
+  extern __shared__ __align__(16) uint8_t q8_dsm[];
+  uint16_t (*wt)[8 * NT][kQ8WRow] = reinterpret_cast<uint16_t (*)[8 * NT][kQ8WRow]>(q8_dsm);
+  int *off = reinterpret_cast<int *>(q8_dsm + sizeof(uint16_t) * kQ8MaxPages * 8 * NT * kQ8WRow);
+  __shared__ float s_red[kQ8Threads];
+  __shared__ float s_m[GP];
+  __shared__ float s_sum[NW][GP];
+  __shared__ int s_page[kQ8MaxPages], s_list[kQ8MaxPages], s_kept[kQ8MaxPages];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  pdl_launch_dependents();
+  const int c = q8_plan(p, off);
+  const long long total = (long long)off[p.B] * p.H;
+  pdl_wait();                                // the logits and maxima of q8_logits
+  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
+    const int u = (int)(item / p.H), h = (int)(item - (long long)u * p.H);
+    const int b = q8_find(off, p.B, u), len = q8_len(p, b);
+    const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
+    __syncthreads();                         // the previous item's shared memory is free
+    if (tid < np) {
+      const int page = p.table[(size_t)b * p.W + p0 + tid];
+      s_page[tid] = page < 0 || page >= p.n_pages ? -1 : page;
+    }
+    // the final maximum of each head over the sequence's items
+    {
+      const int i = tid % GP;
+      float m = -INFINITY;
+      for (int t = off[b] + tid / GP; t < off[b + 1]; t += kQ8Threads / GP)
+        m = fmaxf(m, p.cmax[((long long)t * p.H + h) * GP + i]);
+      s_red[tid] = m;
+    }
+    __syncthreads();
+    if (tid < GP) {
+      float m = s_red[tid];
+      for (int t = tid + GP; t < kQ8Threads; t += GP) m = fmaxf(m, s_red[t]);
+      s_m[tid] = m;
+    }
+    __syncthreads();
+    // weights: warp w takes pages w, w + 4, ..; a lane two keys of a group of four
+    {
+      float sum[GP], m[GP], floor_[GP];
+#pragma unroll
+      for (int i = 0; i < GP; ++i) {
+        sum[i] = 0.f;
+        m[i] = s_m[i];
+        floor_[i] = p.haze > 0.f ? m[i] - p.haze : -INFINITY;
+      }
+      const int key = 4 * (lane >> 1) + (lane & 1);
+      const float *lg = p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0 + key) * GP;
+      for (int pp = warp; pp < np; pp += NW) {
+        const size_t ph = (size_t)max(0, s_page[pp]) * p.H + h;
+        float s[2][GP], vs[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const float4 f = *reinterpret_cast<const float4 *>(lg + (64 * pp + 2 * t) * GP + 4 * i);
+            s[t][4 * i] = f.x; s[t][4 * i + 1] = f.y; s[t][4 * i + 2] = f.z; s[t][4 * i + 3] = f.w;
+          }
+          vs[t] = bf16_bits_to_f32(p.vs[ph * 64 + key + 2 * t]);
+        }
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < GP; ++i) {
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            // a dropped key's weight is a zero whatever its scale holds; a NaN logit is kept
+            const bool keep = i < p.G && !(s[t][i] == -INFINITY || s[t][i] < floor_[i]);
+            any |= keep;
+            const float e = keep ? expf(s[t][i] - m[i]) : 0.f;
+            sum[i] += e;
+            const float w = keep ? e * vs[t] : 0.f;
+            const uint32_t a = f32_to_bf16_rn_bits(w);
+            hi |= a << (16 * t);
+            lo |= (uint32_t)f32_to_bf16_rn_bits(w - bf16_bits_to_f32(a)) << (16 * t);
+          }
+          *reinterpret_cast<uint32_t *>(&wt[pp][2 * i][2 * lane]) = hi;
+          *reinterpret_cast<uint32_t *>(&wt[pp][2 * i + 1][2 * lane]) = lo;
+        }
+        any = __any_sync(0xffffffffu, any);
+        if (lane == 0) s_kept[pp] = any;
+      }
+#pragma unroll
+      for (int i = 0; i < GP; ++i) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        if (lane == 0) s_sum[warp][i] = sum[i];
+      }
+    }
+    __syncthreads();
+    if (tid < GP) {
+      float s = s_sum[0][tid];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) s += s_sum[w][tid];
+      p.psum[item * GP + tid] = s;
+    }
+    // the pages with a weight, in order
+    uint32_t mask = __ballot_sync(0xffffffffu, lane < np && s_kept[lane < np ? lane : 0] != 0);
+    const int n = __popc(mask);
+    if (warp == 0 && (mask >> lane & 1)) s_list[__popc(mask & ((1u << lane) - 1))] = lane;
+    __syncthreads();
+    // warp w: rows (D / 4) w .. of V^T
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.f;
+    const int row = 16 * MT * warp + g;
+    uint4 buf[DEPTH][MT][2];
+    auto issue = [&](int x, uint4 (*dst)[2]) {
+      const size_t ph = (size_t)max(0, s_page[s_list[x]]) * p.H + h;
+      const int8_t *src = p.v + (ph * D + row) * 64 + 16 * tig;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        dst[i][0] = q8_ldg(src + 16 * i * 64);
+        dst[i][1] = q8_ldg(src + (16 * i + 8) * 64);
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (d < n) issue(d, buf[d]);
+    for (int xb = 0; xb < n; xb += DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        const int x = xb + d;
+        if (x >= n) break;
+        const uint16_t (*w)[kQ8WRow] = wt[s_list[x]];
+        uint32_t bw[NT][8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 a = *reinterpret_cast<const uint4 *>(&w[8 * nt + g][16 * tig]);
+          const uint4 e = *reinterpret_cast<const uint4 *>(&w[8 * nt + g][16 * tig + 8]);
+          bw[nt][0] = a.x; bw[nt][1] = a.y; bw[nt][2] = a.z; bw[nt][3] = a.w;
+          bw[nt][4] = e.x; bw[nt][5] = e.y; bw[nt][6] = e.z; bw[nt][7] = e.w;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t r0 = word(buf[d][i][0], s), r1 = word(buf[d][i][1], s);
+            const uint32_t a0 = q8_bf16_pair(r0), a2 = q8_bf16_pair(r0 >> 8);
+            const uint32_t a1 = q8_bf16_pair(r1), a3 = q8_bf16_pair(r1 >> 8);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(acc[i][nt], a0, a1, a2, a3, bw[nt][2 * s], bw[nt][2 * s + 1]);
+          }
+        if (x + DEPTH < n) issue(x + DEPTH, buf[d]);
+      }
+    }
+    // columns 2 tig and 2 tig + 1 are the limbs of one head
+    float *dst = p.pacc + item * p.G * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int head = 4 * nt + tig;
+      if (head < p.G) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          dst[head * D + row + 16 * i] = acc[i][nt][0] + acc[i][nt][1];
+          dst[head * D + row + 16 * i + 8] = acc[i][nt][2] + acc[i][nt][3];
+        }
+      }
+    }
+  }
+}
+
+// out of one query head: the partials of the sequence's items added in order
+// (thread group j the j-th share of them), divided by the sum of the weights.
+template <int D>
+__global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP) {
+  constexpr int NV = D / 4, J = 256 / NV;
+  __shared__ float4 s_acc[J][NV];
+  __shared__ float s_sum[J];
+  const int hq = blockIdx.x, b = blockIdx.y, h = hq / p.G, i = hq - h * p.G;
+  const int v = threadIdx.x % NV, j = threadIdx.x / NV;
+  pdl_wait();
+  const int t0 = p.off[b], nt = p.off[b + 1] - t0;
+  const int a = t0 + (int)((long long)nt * j / J), z = t0 + (int)((long long)nt * (j + 1) / J);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int t = a; t < z; ++t) {
+    const long long item = (long long)t * p.H + h;
+    const float4 x = *reinterpret_cast<const float4 *>(p.pacc + (item * p.G + i) * D + 4 * v);
+    sum += p.psum[item * GP + i];
+    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+  }
+  s_acc[j][v] = acc;
+  if (v == 0) s_sum[j] = sum;
+  __syncthreads();
+  if (j != 0) return;
+#pragma unroll
+  for (int t = 1; t < J; ++t) {
+    const float4 x = s_acc[t][v];
+    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    sum += s_sum[t];
+  }
+  if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);   // no key: zeros
+  else { acc.x /= sum; acc.y /= sum; acc.z /= sum; acc.w /= sum; }
+  const size_t at = ((size_t)b * p.Hq + hq) * D + 4 * v;
+  if (p.out_bf16) {
+    uint2 o;
+    o.x = f32_to_bf16_rn_bits(acc.x) | (uint32_t)f32_to_bf16_rn_bits(acc.y) << 16;
+    o.y = f32_to_bf16_rn_bits(acc.z) | (uint32_t)f32_to_bf16_rn_bits(acc.w) << 16;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = o;
+  } else {
+    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = acc;
+  }
+}
+
+namespace {
+struct Q8Layout {
+  size_t logit, cmax, psum, pacc, off, total;
+  int target;
+  long long items;               // bound on the items of one call
+};
+// Items: sum_b ceil(pages_b / c) H <= N / c + B H <= target r + B H.
+Q8Layout q8_layout(const Q8Shape &s) {
+  Q8Layout y{};
+  const int G = s.Hq / s.Hkv, NT = q8_tiles(G);
+  const long long pages = (s.ctx + 63) / 64;
+  y.target = kQ8Sms * q8_occ(NT);
+  const long long N = pages * s.B * s.Hkv, round = (long long)y.target * kQ8MaxPages;
+  y.items = std::min(N, y.target * ((N + round - 1) / round) + (long long)s.B * s.Hkv);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return o;
+  };
+  y.logit = take((size_t)s.B * s.Hkv * pages * 64 * 4 * NT * 4);
+  y.cmax = take((size_t)y.items * 4 * NT * 4);
+  y.psum = take((size_t)y.items * 4 * NT * 4);
+  y.pacc = take((size_t)y.items * G * s.D * 4);
+  y.off = take((size_t)(s.B + 1) * 4);
+  y.total = at;
+  return y;
+}
+
+size_t q8_pv_smem(int NT, int B) {
+  return sizeof(uint16_t) * kQ8MaxPages * 8 * NT * kQ8WRow + (size_t)(B + 1) * 4;
+}
+
+template <int D, int NT>
+cudaError_t q8_run(const Q8Params &p, long long items, cudaStream_t st, Launcher &L) {
+  const dim3 grid((unsigned)std::min<long long>(items, p.target)), block(kQ8Threads);
+  cudaError_t e = L.launch("q8_logits", q8_logits_kernel<D, NT>, grid, block, (size_t)(p.B + 1) * 4,
+                           st, false, p);
+  if (e != cudaSuccess) return e;
+  e = L.launch("q8_pv", q8_pv_kernel<D, NT>, grid, block, q8_pv_smem(NT, p.B), st, true, p);
+  if (e != cudaSuccess) return e;
+  return L.launch("q8_merge", q8_merge_kernel<D>, dim3((unsigned)p.Hq, (unsigned)p.B), dim3(256), 0,
+                  st, true, p, 4 * NT);
+}
+}  // namespace
+
+size_t q8_workspace_bytes(const Q8Shape &s) { return q8_layout(s).total; }
+
+cudaError_t prepare_q8_kernels() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](const void *k, int NT) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)q8_pv_smem(NT, 4096));
+  };
+  set((const void *)q8_pv_kernel<64, 1>, 1);
+  set((const void *)q8_pv_kernel<64, 2>, 2);
+  set((const void *)q8_pv_kernel<64, 4>, 4);
+  set((const void *)q8_pv_kernel<128, 1>, 1);
+  set((const void *)q8_pv_kernel<128, 2>, 2);
+  set((const void *)q8_pv_kernel<128, 4>, 4);
+  set((const void *)q8_pv_kernel<256, 1>, 1);
+  set((const void *)q8_pv_kernel<256, 2>, 2);
+  set((const void *)q8_pv_kernel<256, 4>, 4);
+  return e;
 }
 
 cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L) {
+  const Q8Layout y = q8_layout(a.s);
+  char *ws = static_cast<char *>(a.workspace);
   Q8Params p{};
   p.q = a.q; p.q_bs = a.q_bs; p.q_hs = a.q_hs;
   p.k = a.pool.k; p.v = a.pool.v; p.ks = a.pool.ks; p.vs = a.pool.vs;
-  p.table = a.pool.table; p.ptable = a.ptable; p.lens = a.lens;
+  p.table = a.pool.table; p.lens = a.lens;
   p.out = a.out; p.out_bf16 = a.out_bf16;
-  p.logit = static_cast<float *>(a.workspace);
+  p.logit = reinterpret_cast<float *>(ws + y.logit);
+  p.cmax = reinterpret_cast<float *>(ws + y.cmax);
+  p.psum = reinterpret_cast<float *>(ws + y.psum);
+  p.pacc = reinterpret_cast<float *>(ws + y.pacc);
+  p.off = reinterpret_cast<int *>(ws + y.off);
   p.B = a.s.B; p.Hq = a.s.Hq; p.H = a.s.Hkv; p.G = a.s.Hq / a.s.Hkv; p.W = a.pool.W;
-  p.n_pages = a.pool.n_pages; p.ctx = a.s.ctx; p.prefix = a.s.prefix; p.ppages = (a.s.prefix + 63) / 64;
+  p.n_pages = a.pool.n_pages; p.ctx = a.s.ctx; p.ctxp = (a.s.ctx + 63) / 64 * 64;
+  p.target = y.target;
   p.scale = a.tau / sqrtf((float)a.s.D);
   p.haze = a.haze;
-  const dim3 gl((unsigned)(p.ppages + (p.ctx + 63) / 64), (unsigned)p.H, (unsigned)p.B);
-  const dim3 go((unsigned)p.Hq, (unsigned)p.B);
-  cudaError_t e;
-#define Q8_CASE(D_)                                                                              \
-  if (a.s.D == D_) {                                                                             \
-    if ((e = L.launch("q8_logits", q8_logits_kernel<D_>, gl, dim3(128), 0, st, false, p)) !=     \
-        cudaSuccess)                                                                             \
-      return e;                                                                                  \
-    return L.launch("q8_out", q8_out_kernel<D_>, go, dim3(D_), 0, st, false, p);                 \
-  }
-  Q8_CASE(64) Q8_CASE(128) Q8_CASE(256)
+  const int NT = q8_tiles(p.G);
+#define Q8_CASE(D_, N_) \
+  if (a.s.D == D_ && NT == N_) return q8_run<D_, N_>(p, y.items, st, L);
+  Q8_CASE(64, 1) Q8_CASE(64, 2) Q8_CASE(64, 4)
+  Q8_CASE(128, 1) Q8_CASE(128, 2) Q8_CASE(128, 4)
+  Q8_CASE(256, 1) Q8_CASE(256, 2) Q8_CASE(256, 4)
 #undef Q8_CASE
   return cudaErrorInvalidValue;
 }

@@ -83,6 +83,7 @@ dvssq_status ensure_device() {
   if ((e = prepare_stack_kernels()) != cudaSuccess) return cuda_fail(e);
   if ((e = prepare_materialize_kernels()) != cudaSuccess) return cuda_fail(e);
   if ((e = prepare_lowrank_kernels()) != cudaSuccess) return cuda_fail(e);
+  if ((e = prepare_q8_kernels()) != cudaSuccess) return cuda_fail(e);
   ready[dev] = 1;
   return DVSSQ_OK;
 }
@@ -458,7 +459,7 @@ dvssq_status q8_size(const dvssq_attn_shape *shape, int32_t prefix_len, size_t *
   Q8Shape qs{};
   const dvssq_status s = q8_shape(shape, prefix_len, qs);
   if (s != DVSSQ_OK) return s;
-  *bytes = q8_workspace_bytes(qs);
+  *bytes = prefix_len > 0 ? pfx_workspace_bytes(qs) : q8_workspace_bytes(qs);
   return DVSSQ_OK;
 }
 
@@ -483,7 +484,9 @@ dvssq_status q8_attention(const dvssq_attn_shape *shape, const dvssq_kv_cache *c
   for (const void *b : bufs)
     if (!aligned16(b)) return DVSSQ_ERR_MISALIGNED;
   if (!aligned256(workspace)) return DVSSQ_ERR_MISALIGNED;
-  if (workspace_bytes < q8_workspace_bytes(a.s)) return DVSSQ_ERR_WORKSPACE;
+  // without a prefix both entry points run the decode form
+  const size_t need = prefix_len > 0 ? pfx_workspace_bytes(a.s) : q8_workspace_bytes(a.s);
+  if (workspace_bytes < need) return DVSSQ_ERR_WORKSPACE;
   if ((s = ensure_device()) != DVSSQ_OK) return s;
   a.q = static_cast<const uint16_t *>(q);
   a.q_bs = q_bs; a.q_hs = q_hs;
@@ -491,7 +494,9 @@ dvssq_status q8_attention(const dvssq_attn_shape *shape, const dvssq_kv_cache *c
   a.tau = shape->tau; a.haze = shape->haze;
   a.out = out; a.out_bf16 = y_dtype == DVSSQ_Y_BF16;
   a.workspace = workspace;
-  const cudaError_t e = launch_q8_attention(a, static_cast<cudaStream_t>(stream), launcher());
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = prefix_len > 0 ? launch_prefix_attention(a, st, launcher())
+                                       : launch_q8_attention(a, st, launcher());
   return e == cudaSuccess ? DVSSQ_OK : cuda_fail(e);
 }
 }  // namespace

@@ -257,6 +257,9 @@ struct Q8Args {
 };
 size_t q8_workspace_bytes(const Q8Shape &s);
 cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L);
+cudaError_t prepare_q8_kernels();
+size_t pfx_workspace_bytes(const Q8Shape &s);
+cudaError_t launch_prefix_attention(const Q8Args &a, cudaStream_t st, Launcher &L);
 
 // Tensor-map encoder from the driver (resolved once through the runtime).
 CUresult encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
