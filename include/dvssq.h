@@ -25,7 +25,8 @@
  * - Matrices are dense and row-major.  BF16 values travel as uint16_t bit
  *   patterns.
  * - Every device buffer must be 16-byte aligned (cudaMalloc gives 256 B);
- *   the workspace must be 256-byte aligned.  Violations return
+ *   the workspace must be 256-byte aligned, and the int32 index arrays of
+ *   the KV-cache calls need 4 bytes only.  Violations return
  *   DVSSQ_ERR_MISALIGNED before any launch.
  * - Calls are asynchronous and stream-ordered on `stream` (a cudaStream_t;
  *   NULL is the legacy default stream).  Argument validation happens on the

@@ -52,9 +52,24 @@ struct Q8Params {
   float *cmax, *psum;            // [items][4 NT]
   float *pacc;                   // [items][G][D]
   int *off;                      // [B + 1] first item of each sequence (per KV head)
+  // a shared prefix (splits > 0): its row maxima, its largest value scale per KV
+  // head, and its splits' partial sums, rows = B G per KV head
+  uint32_t *mrow, *svmax;
+  const float *po, *pl;
+  int splits, rows;
   int B, Hq, H, G, W, n_pages, ctx, ctxp, target;
   float scale, haze;
 };
+
+// FP32 bits in an order-preserving unsigned form, for an atomic maximum; 0 (no
+// value's form) reads as -inf.
+__device__ __forceinline__ uint32_t order_bits(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float from_order_bits(uint32_t u) {
+  return u == 0 ? -INFINITY : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
 
 __device__ __forceinline__ int q8_len(const Q8Params &p, int b) {
   const int n = p.lens[b];
@@ -194,6 +209,11 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
   const int c = q8_plan(p, off);
   if (blockIdx.x == 0)
     for (int b = tid; b <= p.B; b += kQ8Threads) p.off[b] = off[b];
+  if (p.splits > 0) {
+    // the prefix kernels raise these by atomic maxima (0 lies below every value)
+    for (int i = blockIdx.x * kQ8Threads + tid; i < p.B * p.Hq; i += gridDim.x * kQ8Threads) p.mrow[i] = 0;
+    for (int i = blockIdx.x * kQ8Threads + tid; i < p.H; i += gridDim.x * kQ8Threads) p.svmax[i] = 0;
+  }
   const long long total = (long long)off[p.B] * p.H;
   int held = -1;                             // the (sequence, KV head) whose limbs are held
   uint32_t qf[NT][DB][4];
@@ -354,6 +374,8 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
     if (tid < GP) {
       float m = s_red[tid];
       for (int t = tid + GP; t < kQ8Threads; t += GP) m = fmaxf(m, s_red[t]);
+      if (p.splits > 0 && tid < p.G)
+        m = fmaxf(m, from_order_bits(p.mrow[(size_t)b * p.Hq + h * p.G + tid]));
       s_m[tid] = m;
     }
     __syncthreads();
@@ -487,8 +509,9 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
   }
 }
 
-// out of one query head: the partials of the sequence's items added in order
-// (thread group j the j-th share of them), divided by the sum of the weights.
+// out of one query head: the partials of the sequence's items, then those of the
+// prefix's splits, added in order (thread group j the j-th share of them),
+// divided by the sum of the weights.
 template <int D>
 __global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP) {
   constexpr int NV = D / 4, J = 256 / NV;
@@ -497,15 +520,17 @@ __global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP)
   const int hq = blockIdx.x, b = blockIdx.y, h = hq / p.G, i = hq - h * p.G;
   const int v = threadIdx.x % NV, j = threadIdx.x / NV;
   pdl_wait();
-  const int t0 = p.off[b], nt = p.off[b + 1] - t0;
-  const int a = t0 + (int)((long long)nt * j / J), z = t0 + (int)((long long)nt * (j + 1) / J);
+  const int t0 = p.off[b], own = p.off[b + 1] - t0, nt = own + p.splits;
+  const int a = (int)((long long)nt * j / J), z = (int)((long long)nt * (j + 1) / J);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
 #pragma unroll 4
   for (int t = a; t < z; ++t) {
-    const long long item = (long long)t * p.H + h;
-    const float4 x = *reinterpret_cast<const float4 *>(p.pacc + (item * p.G + i) * D + 4 * v);
-    sum += p.psum[item * GP + i];
+    const long long item = (long long)(t0 + t) * p.H + h;
+    const long long row = ((long long)(t - own) * p.H + h) * p.rows + (long long)b * p.G + i;
+    const float *src = t < own ? p.pacc + (item * p.G + i) * D : p.po + row * D;
+    const float4 x = *reinterpret_cast<const float4 *>(src + 4 * v);
+    sum += t < own ? p.psum[item * GP + i] : p.pl[row];
     acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
   }
   s_acc[j][v] = acc;
@@ -598,8 +623,8 @@ cudaError_t prepare_q8_kernels() {
   return e;
 }
 
-cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L) {
-  const Q8Layout y = q8_layout(a.s);
+namespace {
+Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
   char *ws = static_cast<char *>(a.workspace);
   Q8Params p{};
   p.q = a.q; p.q_bs = a.q_bs; p.q_hs = a.q_hs;
@@ -616,6 +641,13 @@ cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L) {
   p.target = y.target;
   p.scale = a.tau / sqrtf((float)a.s.D);
   p.haze = a.haze;
+  return p;
+}
+}  // namespace
+
+cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L) {
+  const Q8Layout y = q8_layout(a.s);
+  const Q8Params p = q8_params(a, y);
   const int NT = q8_tiles(p.G);
 #define Q8_CASE(D_, N_) \
   if (a.s.D == D_ && NT == N_) return q8_run<D_, N_>(p, y.items, st, L);

@@ -40,6 +40,7 @@ dvssq_status cuda_fail(cudaError_t e) {
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 // Shape rules shared by every entry point (see dvssq_shape in dvssq.h).
@@ -84,6 +85,7 @@ dvssq_status ensure_device() {
   if ((e = prepare_materialize_kernels()) != cudaSuccess) return cuda_fail(e);
   if ((e = prepare_lowrank_kernels()) != cudaSuccess) return cuda_fail(e);
   if ((e = prepare_q8_kernels()) != cudaSuccess) return cuda_fail(e);
+  if ((e = prepare_prefix_kernels()) != cudaSuccess) return cuda_fail(e);
   ready[dev] = 1;
   return DVSSQ_OK;
 }
@@ -412,9 +414,10 @@ dvssq_status kv_pool(const dvssq_kv_cache *c, KvPool &p) {
   if (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
       c->table == nullptr)
     return DVSSQ_ERR_INVALID_ARG;
-  const void *bufs[] = {c->k, c->v, c->k_scale, c->v_scale, c->table};
+  const void *bufs[] = {c->k, c->v, c->k_scale, c->v_scale};
   for (const void *b : bufs)
     if (!aligned16(b)) return DVSSQ_ERR_MISALIGNED;
+  if (!aligned4(c->table)) return DVSSQ_ERR_MISALIGNED;
   p.k = c->k; p.v = c->v; p.ks = c->k_scale; p.vs = c->v_scale; p.table = c->table;
   p.n_pages = c->n_pages; p.H = c->kv_heads; p.D = c->head_dim; p.B = c->batch;
   p.W = c->table_width;
@@ -435,7 +438,7 @@ dvssq_status kv_rows(const dvssq_kv_cache *c, int64_t tokens, const int32_t *sta
   if (tokens < 0 || tokens > ((int64_t)1 << 30)) return DVSSQ_ERR_INVALID_ARG;
   if (tokens == 0) return DVSSQ_OK;
   if (start == nullptr || (cu == nullptr && tokens != c->batch)) return DVSSQ_ERR_INVALID_ARG;
-  if (!aligned16(start) || !aligned16(cu)) return DVSSQ_ERR_MISALIGNED;
+  if (!aligned4(start) || !aligned4(cu)) return DVSSQ_ERR_MISALIGNED;
   return DVSSQ_OK;
 }
 
@@ -480,9 +483,8 @@ dvssq_status q8_attention(const dvssq_attn_shape *shape, const dvssq_kv_cache *c
     return DVSSQ_ERR_INVALID_ARG;
   if (y_dtype != DVSSQ_Y_F32 && y_dtype != DVSSQ_Y_BF16) return DVSSQ_ERR_INVALID_ARG;
   if ((s = kv_strides(q_bs, q_hs)) != DVSSQ_OK) return s;
-  const void *bufs[] = {q, lens, out, prefix_len > 0 ? prefix_table : nullptr};
-  for (const void *b : bufs)
-    if (!aligned16(b)) return DVSSQ_ERR_MISALIGNED;
+  if (!aligned16(q) || !aligned16(out)) return DVSSQ_ERR_MISALIGNED;
+  if (!aligned4(lens) || (prefix_len > 0 && !aligned4(prefix_table))) return DVSSQ_ERR_MISALIGNED;
   if (!aligned256(workspace)) return DVSSQ_ERR_MISALIGNED;
   // without a prefix both entry points run the decode form
   const size_t need = prefix_len > 0 ? pfx_workspace_bytes(a.s) : q8_workspace_bytes(a.s);

@@ -258,6 +258,7 @@ struct Q8Args {
 size_t q8_workspace_bytes(const Q8Shape &s);
 cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L);
 cudaError_t prepare_q8_kernels();
+cudaError_t prepare_prefix_kernels();
 size_t pfx_workspace_bytes(const Q8Shape &s);
 cudaError_t launch_prefix_attention(const Q8Args &a, cudaStream_t st, Launcher &L);
 

@@ -411,6 +411,23 @@ def test_shared_prefix_loop(dv):
     assert same_bits(vo, vp.transpose(0, 1).float().to(torch.bfloat16).contiguous())
 
 
+def test_index_arrays_may_be_slices(dv):
+    """Index arrays at any 4-byte offset, as slices of one tensor give them."""
+    lens, prefix = [70, 0, 5], 100
+    q = P.queries(3, 8, 64, seed=85)
+    pool, table, ptable = P.filled(3, 2, 64, lens, seed=86, prefix=prefix)
+    flat = torch.cat([i32([0]), table.reshape(-1).cuda(), i32([0]), ptable.cuda(), i32([0] + lens)])
+    at, W = 1, table.shape[1]
+    views = []
+    for n in (3 * W, 2, 3):
+        views.append(flat[at: at + n])
+        at += n + 1
+    assert all(x.data_ptr() % 16 for x in views[:2])
+    c = dv.KvCache(*(pool[n].cuda() for n in ("k", "v", "ks", "vs")), views[0].view(3, W))
+    out = dv.dvssq_bss_attention_prefix(q.cuda(), c, views[2], views[1], prefix)
+    check(out, P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix), PREFIX)
+
+
 def test_two_streams_and_explicit_streams(dv):
     """Calls on two streams at once, each with its own workspace, give what one stream gives."""
     lens = [1200, 700]

@@ -38,7 +38,7 @@ BAD_CACHES = [
     (dict(batch=0), 2), (dict(batch=4097), 2), (dict(n_pages=0), 2), (dict(table_width=0), 2),
     (dict(table_width=2 ** 18 + 1), 2), (dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1),
     (dict(v_scale=None), 1), (dict(table=None), 1), (dict(k=264), 3), (dict(v=264), 3),
-    (dict(k_scale=258), 3), (dict(v_scale=258), 3), (dict(table=260), 3),
+    (dict(k_scale=258), 3), (dict(v_scale=258), 3), (dict(table=258), 3),
 ]
 
 
@@ -61,9 +61,9 @@ def test_append_and_read_argument_checks(dv):
     assert append(dv, c, kts=-8) == 1 and append(dv, c, vhs=-8) == 1
     assert append(dv, c, kts=516) == 3 and append(dv, c, khs=4) == 3 and append(dv, c, vts=2) == 3
     assert append(dv, c, k=264) == 3 and append(dv, c, v=264) == 3
-    assert append(dv, c, start=260) == 3 and append(dv, c, T=7, cu=264) == 3
+    assert append(dv, c, start=258) == 3 and append(dv, c, T=7, cu=262) == 3
     assert read(dv, c, k=None) == 1 and read(dv, c, v=None) == 1
-    assert read(dv, c, k=264) == 3 and read(dv, c, v=264) == 3 and read(dv, c, start=260) == 3
+    assert read(dv, c, k=264) == 3 and read(dv, c, v=264) == 3 and read(dv, c, start=258) == 3
 
 
 def attend(dv, c, shape=None, q=256, qbs=2048, qhs=128, lens=256, out=256, yd=0, ws=256, wsb=1 << 40,
@@ -107,11 +107,11 @@ def test_attention_argument_checks(dv):
         assert call(q=None) == 1 and call(lens=None) == 1 and call(out=None) == 1 and call(ws=None) == 1
         assert call(yd=2) == 1 and call(qbs=-8) == 1
         assert call(qbs=2044) == 3 and call(qhs=100) == 3
-        assert call(q=264) == 3 and call(lens=260) == 3 and call(out=264) == 3 and call(ws=272) == 3
+        assert call(q=264) == 3 and call(lens=258) == 3 and call(out=264) == 3 and call(ws=272) == 3
         assert call(wsb=need - 256) == 4
     assert attend(dv, c, entry="prefix", plen=-1, prefix=256) == 1
     assert attend(dv, c, entry="prefix", plen=100, prefix=None) == 1
-    assert attend(dv, c, entry="prefix", plen=100, prefix=264) == 3
+    assert attend(dv, c, entry="prefix", plen=100, prefix=262) == 3
     assert attend(dv, c, entry="prefix", plen=5000, prefix=256, wsb=need) == 4
 
 
