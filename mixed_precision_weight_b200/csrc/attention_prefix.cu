@@ -10,13 +10,13 @@
 // Each sequence's own keys go through q8_logits and q8_pv as without a prefix,
 // and q8_merge adds the items' and the splits' partials in order.
 //
-// A CTA holds 128 rows of Q and walks a split of the prefix in steps of two
-// pages (128 keys).  Warps 0-7 turn S into weights (a warpgroup per page of the
-// step, a thread per row), warps 8-11 bring K and warps 12-15 V from global
-// memory through registers, where the 8-bit codes become FP16, into
-// 128-byte-swizzled shared memory, and one thread issues the MMAs.  S is
-// double-buffered in tensor memory; Q K^T of step i + 1 is issued before w V of
-// step i, so that the weights of a step are formed behind the next product.
+// A CTA holds 128 rows of Q and walks a split of the prefix page by page (64
+// keys).  Warps 0-3 turn S into weights (a thread per row), warps 4-7 bring K
+// and warps 8-11 V from global memory through registers, two pages ahead, where
+// the 8-bit codes become FP16, into 128-byte-swizzled shared memory, and one
+// thread of warp 12 issues the MMAs.  Four S buffers in tensor memory; Q K^T of
+// page j is issued before w V of page j - 2, so that a page's weights are formed
+// behind two products.
 //
 // Number formats: a code is exact in FP16 (1024 + u from a byte permutation,
 // minus 1152), and so is a query scaled by a power of two to 2^14 .. 2^15 (BF16
@@ -29,14 +29,14 @@
 
 namespace dvssq {
 
-constexpr int kPfxThreads = 17 * 32;
-constexpr int kPfxSoft = 256;            // threads of the weight warps
+constexpr int kPfxThreads = 13 * 32;
+constexpr int kPfxAhead = 2;             // pages of Q K^T issued ahead of w V
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct PfxParams {
   Q8Params q8;
   const int32_t *ptable;
-  int prefix, pages, steps, splits, rows;   // rows = B G per KV head
+  int prefix, pages, splits, rows;          // rows = B G per KV head
   uint32_t *mrow;                // [B][Hq] row maxima, order-preserving bits
   uint32_t *svmax;               // [H] largest finite value scale (bits)
   float *po;                     // [splits][H][rows][D]
@@ -53,6 +53,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
         "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+// Waits for the thread's tensor-memory loads; the values pass through, so that no
+// use of them can be placed before the wait.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t r[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]) : : "memory");
 }
 
 // 16 codes -> 16 FP16 values in order, as two 16-byte chunks
@@ -82,89 +96,102 @@ __device__ __forceinline__ float ex2_approx(float x) {
 template <int D, bool PV>
 struct PfxSmem {
   static constexpr int DB = D / 64;
-  static constexpr int NK = !PV || D < 256 ? 2 : 1;      // K slots (128 keys each)
+  static constexpr int NK = !PV || D < 256 ? 4 : 2;      // K slots (a page each)
+  static constexpr int kPage = DB * 64 * 128;            // FP16 K page: DB blocks of 64 rows x 128 bytes
   static constexpr int kTile = 128 * 128;                // 128 rows of 128 bytes
-  static constexpr int kV = D * 128;                     // one page of V
+  static constexpr int kV = D * 128;                     // FP16 V page: D rows of 128 bytes
   static constexpr int q = 0;
   static constexpr int k = q + DB * kTile;
-  static constexpr int v = k + NK * DB * kTile;
+  static constexpr int v = k + NK * kPage;
   static constexpr int w = v + (PV ? 2 * kV : 0);
-  static constexpr int sc = w + (PV ? 2 * kTile : 0);    // float2 [2][128]: key and value scales
-  static constexpr int step = sc + 2 * 128 * 8;          // float [128]
-  static constexpr int nv = step + 128 * 4;              // int [2][2]: live keys of each page
-  static constexpr int bar = nv + 16;
-  static constexpr int bytes = bar + 20 * 8 + 16;
+  static constexpr int sa = w + (PV ? 2 * kTile : 0);    // float [4][64]: key scales
+  static constexpr int sv = sa + 4 * 64 * 4;             // float [4][64]: value scales
+  static constexpr int step = sv + 4 * 64 * 4;           // float [128]
+  static constexpr int nv = step + 128 * 4;              // int [4][2]: live keys, NaN value scales
+  static constexpr int bar = nv + 32;
+  static constexpr int bytes = bar + 27 * 8 + 16;
 };
 
 template <int D, bool PV>
 __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) {
   using L = PfxSmem<D, PV>;
-  constexpr int DB = L::DB, NK = L::NK;
+  constexpr int DB = L::DB, NK = L::NK, VPL = D / 32;
   extern __shared__ __align__(1024) uint8_t pfx_sm[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(pfx_sm + L::bar);
-  uint64_t *k_full = bar, *k_empty = bar + 2, *s_full = bar + 4, *s_empty = bar + 6,
-           *sc_full = bar + 8, *v_full = bar + 10, *v_empty = bar + 12, *w_full = bar + 14,
-           *w_empty = bar + 15, *o_full = bar + 16;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 20);
-  float2 (*sc)[128] = reinterpret_cast<float2 (*)[128]>(pfx_sm + L::sc);
+  uint64_t *k_full = bar, *k_empty = bar + 4, *s_full = bar + 8, *s_empty = bar + 12,
+           *sc_full = bar + 16, *v_full = bar + 20, *v_empty = bar + 22, *w_full = bar + 24,
+           *o_full = bar + 26;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 27);
+  float (*s_a)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sa);
+  float (*s_v)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sv);
   float *s_step = reinterpret_cast<float *>(pfx_sm + L::step);
   int (*s_nv)[2] = reinterpret_cast<int (*)[2]>(pfx_sm + L::nv);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, h = blockIdx.y, rt = blockIdx.z;
   const int H = p.q8.H, G = p.q8.G;
-  const int i0 = (int)((long long)p.steps * split / p.splits);
-  const int n = (int)((long long)p.steps * (split + 1) / p.splits) - i0;
+  const int j0 = (int)((long long)p.pages * split / p.splits);
+  const int n = (int)((long long)p.pages * (split + 1) / p.splits) - j0;
   if ((smem_u32(pfx_sm) & 1023) != 0) {      // the swizzled tiles need it; the segment's alignment gives it
     if (tid == 0) set_error(kErrBadShape);
     return;
   }
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&k_full[s], 4);
       mbar_init(&k_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&s_empty[s], 8);
+      mbar_init(&s_empty[s], 4);
       mbar_init(&sc_full[s], 4);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&v_full[s], 4);
       mbar_init(&v_empty[s], 1);
+      mbar_init(&w_full[s], 4);
     }
-    mbar_init(w_full, 8);
-    mbar_init(w_empty, 1);
     mbar_init(o_full, 1);
     fence_mbarrier_init();
   }
-  if (warp == 16) {
+  if (warp == 12) {
     tmem_alloc(tmem_slot, PV ? 512 : 256);
     tmem_relinquish();
   }
-  // Q: a warp per row; row r of the tile is query head h G + r % G of sequence r / G
-  for (int r = warp; r < 128; r += 17) {
-    constexpr int VPL = D / 32;
-    const int rr = rt * 128 + r;
-    uint32_t bits[VPL], m = 0;
+  // Q: a warp per row, five rows in flight; row r of the tile is query head
+  // h G + r % G of sequence r / G
+#pragma unroll 1
+  for (int r0 = warp; r0 < 128; r0 += 5 * 13) {
+    KvRaw<VPL> raw[5];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) bits[i] = 0;
-    if (rr < p.rows) {
-      const int b = rr / G;
-      const uint16_t *src = p.q8.q + b * p.q8.q_bs + (long long)(h * G + rr - b * G) * p.q8.q_hs + lane * VPL;
+    for (int u = 0; u < 5; ++u) {
+      const int r = r0 + 13 * u, rr = rt * 128 + r;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        bits[i] = src[i];
-        m = max(m, bits[i] & 0x7FFFu);
+      for (int i = 0; i < VPL / 2; ++i) raw[u].w[i] = 0;
+      if (r < 128 && rr < p.rows) {
+        const int b = rr / G;
+        raw[u] = kv_load<VPL>(p.q8.q + b * p.q8.q_bs + (long long)(h * G + rr - b * G) * p.q8.q_hs + lane * VPL);
       }
     }
-    m = __reduce_max_sync(0xffffffffu, m);
-    const int e = max((int)(m >> 7) - 127, -126);
-    uint16_t f[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      f[i] = m >= 0x7F80u ? 0 : __half_as_ushort(__float2half_rn(ldexpf(bf16_bits_to_f32(bits[i]), 14 - e)));
-    const int dim = lane * VPL, kb = dim >> 6, c = (dim & 63) >> 3;
-    uint16_t *dst = reinterpret_cast<uint16_t *>(pfx_sm + L::q + kb * L::kTile + r * 128 + ((c ^ (r & 7)) << 4)) + (dim & 7);
+    for (int u = 0; u < 5; ++u) {
+      const int r = r0 + 13 * u;
+      if (r >= 128) break;
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; i += 2)
-      *reinterpret_cast<uint32_t *>(dst + i) = f[i] | (uint32_t)f[i + 1] << 16;
-    if (lane == 0) s_step[r] = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, e - 14);
+      for (int i = 0; i < VPL / 2; ++i) m = max(m, max(raw[u].w[i] & 0x7FFFu, (raw[u].w[i] >> 16) & 0x7FFFu));
+      m = __reduce_max_sync(0xffffffffu, m);
+      const bool finite = m < 0x7F80u;
+      // times 2^(14 - e) in two exact steps (14 - e is 140 at most)
+      const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100);
+      const float f0 = __int_as_float((up + 127) << 23), f1 = __int_as_float((14 - e - up + 127) << 23);
+      const int dim = lane * VPL, kb = dim >> 6, c = (dim & 63) >> 3;
+      uint8_t *dst = pfx_sm + L::q + kb * L::kTile + r * 128 + ((c ^ (r & 7)) << 4) + 2 * (dim & 7);
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) {
+        const __half2 x = __floats2half2_rn(bf16_bits_to_f32(raw[u].w[i] & 0xFFFFu) * f0 * f1,
+                                            bf16_bits_to_f32(raw[u].w[i] >> 16) * f0 * f1);
+        *reinterpret_cast<uint32_t *>(dst + 4 * i) = finite ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+      }
+      if (lane == 0) s_step[r] = finite ? ldexpf(1.0f, e - 14) : __uint_as_float(0x7FC00000u);
+    }
   }
   fence_proxy_async_smem();
   tc_fence_before();
@@ -175,14 +202,15 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
-  if (warp < 8) {
+  if (warp < 4) {
     // ------------------------------- weights -------------------------------
-    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane, rr = rt * 128 + row;
+    const int row = tid, rr = rt * 128 + row;
     const bool live = rr < p.rows;
     const int b = live ? rr / G : 0, hq = h * G + (live ? rr - b * G : 0);
     const float r1 = s_step[row] * p.q8.scale;       // logit = S ks r1
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    float mx = -INFINITY, sum = 0.f, x0 = 0.f, floor2 = -INFINITY;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    float mx = -INFINITY, x0 = 0.f, floor2 = -INFINITY;
+    float2 sum = make_float2(0.f, 0.f);
     int shift = 0;
     if constexpr (PV) {
       pdl_wait();                                    // the row maxima, of the prefix and of the items
@@ -190,7 +218,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       const int gp = 4 * q8_tiles(G);
       for (int t = p.q8.off[b]; t < p.q8.off[b + 1]; ++t)
         m = fmaxf(m, p.q8.cmax[((long long)t * H + h) * gp + hq - h * G]);
-      // weights times 2^shift: the largest vs 2^shift lies in (2^13, 2^14]
+      // weights times 2^shift: the largest vs 2^shift lies in [2^13, 2^14)
       const uint32_t sv = p.svmax[h];
       if (sv != 0) {
         int e;
@@ -203,67 +231,86 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     }
     const float r2 = r1 * kLog2e;
-    for (int i = 0; i < n && ok; ++i) {
-      const int sb = i & 1, par = (i >> 1) & 1;
+    for (int j = 0; j < n && ok; ++j) {
+      const int sb = j & 3, par = (j >> 2) & 1;
       bool got = mbar_wait(&sc_full[sb], par) && mbar_wait(&s_full[sb], par);
       if constexpr (PV)
-        if (i > 0) got = got && mbar_wait(w_empty, (i - 1) & 1);
+        if (j >= 2) got = got && mbar_wait(&v_empty[j & 1], ((j >> 1) - 1) & 1);   // the slot's w V is done
       // a warp gives up as one: the tensor-memory loads are warp-wide
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
-      const int nv = s_nv[sb][half];
-      const float2 *scale = sc[sb] + 64 * half;
-      const uint32_t src = lane_base + (PV ? 256 : 0) + 128 * sb + 64 * half;
+      const int nv = s_nv[sb][0];
+      const bool plain = nv == 64 && (s_nv[sb][1] == 0);
+      const uint32_t src = lane_base + (PV ? 256 : 0) + 64 * sb;
+      uint32_t s[64];
+      tmem_ld32(src, s);
+      tmem_ld32(src + 32, s + 32);
+      tmem_ld_wait32(s);
+      tmem_ld_wait32(s + 32);
+      if constexpr (!PV) {
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t s[32];
-        tmem_ld32(src + 32 * cc, s);
-        tmem_ld_wait();
-        if constexpr (!PV) {
-          float f[32];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float4 a = *reinterpret_cast<const float4 *>(&scale[32 * cc + j]);
-            f[j] = __uint_as_float(s[j]) * a.x;
-            f[j + 1] = __uint_as_float(s[j + 1]) * a.z;
-          }
+        for (int i = 0; i < 64; i += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(&s_a[sb][i]);
+          const float2 x = mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y));
+          const float2 y = mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w));
           if (nv == 64) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, f[j]);
+            mx = fmaxf(fmaxf(mx, fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
           } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * cc + j < nv) mx = fmaxf(mx, f[j]);
+            if (i < nv) mx = fmaxf(mx, x.x);
+            if (i + 1 < nv) mx = fmaxf(mx, x.y);
+            if (i + 2 < nv) mx = fmaxf(mx, y.x);
+            if (i + 3 < nv) mx = fmaxf(mx, y.y);
           }
-        } else {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float4 a = *reinterpret_cast<const float4 *>(&scale[32 * cc + j]);
-            const float x = fmaf(__uint_as_float(s[j]) * a.x, r2, x0);
-            const float y = fmaf(__uint_as_float(s[j + 1]) * a.z, r2, x0);
-            // a NaN logit is kept; a dropped key's value scale is not looked at
-            const bool kx = !(x < floor2) && (nv == 64 || 32 * cc + j < nv);
-            const bool ky = !(y < floor2) && (nv == 64 || 32 * cc + j + 1 < nv);
-            const float ex = kx ? ex2_approx(x) : 0.f, ey = ky ? ex2_approx(y) : 0.f;
-            sum += ex;
-            sum += ey;
-            const __half2 o = __floats2half2_rn(kx ? ex * a.y : 0.f, ky ? ey * a.w : 0.f);
-            w[j / 2] = *reinterpret_cast<const uint32_t *>(&o);
-          }
-          uint8_t *dst = pfx_sm + L::w + half * L::kTile + row * 128;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(dst + (((4 * cc + j) ^ (row & 7)) << 4)) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
+      } else {
+        uint8_t *dst = pfx_sm + L::w + (j & 1) * L::kTile + row * 128;
+        const float2 rr2 = make_float2(r2, r2), xx0 = make_float2(x0, x0);
+#pragma unroll
+        for (int i = 0; i < 64; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int t = 0; t < 8; t += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(&s_a[sb][i + t]);
+            const float4 v = *reinterpret_cast<const float4 *>(&s_v[sb][i + t]);
+            const float2 x = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + t]), __uint_as_float(s[i + t + 1])),
+                                               make_float2(a.x, a.y)), rr2, xx0);
+            const float2 y = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + t + 2]), __uint_as_float(s[i + t + 3])),
+                                               make_float2(a.z, a.w)), rr2, xx0);
+            float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            float2 ey = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            float2 wx, wy;
+            // a NaN logit is kept
+            if (x.x < floor2) ex.x = 0.f;
+            if (x.y < floor2) ex.y = 0.f;
+            if (y.x < floor2) ey.x = 0.f;
+            if (y.y < floor2) ey.y = 0.f;
+            if (plain) {
+              wx = mat_mul2(ex, make_float2(v.x, v.y));
+              wy = mat_mul2(ey, make_float2(v.z, v.w));
+            } else {
+              // keys past the prefix's end weigh nothing, and the value scale of a key
+              // without weight is not looked at
+              if (i + t >= nv) ex.x = 0.f;
+              if (i + t + 1 >= nv) ex.y = 0.f;
+              if (i + t + 2 >= nv) ey.x = 0.f;
+              if (i + t + 3 >= nv) ey.y = 0.f;
+              wx = make_float2(ex.x == 0.f ? 0.f : ex.x * v.x, ex.y == 0.f ? 0.f : ex.y * v.y);
+              wy = make_float2(ey.x == 0.f ? 0.f : ey.x * v.z, ey.y == 0.f ? 0.f : ey.y * v.w);
+            }
+            sum = mat_add2(sum, mat_add2(ex, ey));
+            const __half2 ox = __floats2half2_rn(wx.x, wx.y), oy = __floats2half2_rn(wy.x, wy.y);
+            w[t / 2] = *reinterpret_cast<const uint32_t *>(&ox);
+            w[t / 2 + 1] = *reinterpret_cast<const uint32_t *>(&oy);
+          }
+          *reinterpret_cast<uint4 *>(dst + (((i >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
       }
-      if constexpr (PV) fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&s_empty[sb]);
-        if constexpr (PV) mbar_arrive(w_full);
+        if constexpr (PV) mbar_arrive(&w_full[j & 1]);
       }
     }
     if constexpr (!PV) {
@@ -271,173 +318,197 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       const float m = mx * r1;
       if (live && m == m) atomicMax(&p.mrow[(size_t)b * p.q8.Hq + hq], order_bits(m));
     } else {
-      if (ok && !mbar_wait(o_full, 0)) ok = false;
+      if (!__all_sync(0xffffffffu, ok && mbar_wait(o_full, 0))) ok = false;
       tc_fence_after();
       const float back = ldexpf(1.0f, -shift);
-      const size_t at = ((size_t)split * H + h) * p.rows + rr;
+      const size_t at = ((size_t)split * H + h) * p.rows;
+      if (live) p.pl[at + rr] = (sum.x + sum.y) * back;
+      // 32 x 32 blocks through shared memory (K's, free now): whole 128-byte lines out
+      float (*st)[36] = reinterpret_cast<float (*)[36]>(pfx_sm + L::k + warp * 32 * 36 * 4);
+      const int sub = lane >> 3, c4 = (lane & 7) * 4;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 64; ++cc) {
+      for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
-        const int col = half * (D / 2) + 32 * cc;
-        tmem_ld32(lane_base + col, o);
-        tmem_ld_wait();
-        if (live && ok) {
+        tmem_ld32(lane_base + 32 * cc, o);
+        tmem_ld_wait32(o);
+        __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4 *>(p.po + at * D + col + j) =
-                make_float4(__uint_as_float(o[j]) * back, __uint_as_float(o[j + 1]) * back,
-                            __uint_as_float(o[j + 2]) * back, __uint_as_float(o[j + 3]) * back);
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<float4 *>(&st[lane][i]) =
+              make_float4(__uint_as_float(o[i]) * back, __uint_as_float(o[i + 1]) * back,
+                          __uint_as_float(o[i + 2]) * back, __uint_as_float(o[i + 3]) * back);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rw = 4 * i + sub, gr = rt * 128 + 32 * warp + rw;
+          if (gr < p.rows && ok)
+            *reinterpret_cast<float4 *>(p.po + (at + gr) * D + 32 * cc + c4) =
+                *reinterpret_cast<const float4 *>(&st[rw][c4]);
         }
       }
       tc_fence_before();
-      // the two halves' sums of the row
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (half == 1) s_step[row] = sum;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (half == 0 && live) p.pl[at] = (sum + s_step[row]) * back;
     }
-  } else if (warp < 12) {
+  } else if (warp < 8) {
     // -------------------------------- K and scales --------------------------------
-    const int kt = tid - 256;
-    constexpr int NL = D / 16;                       // 16-byte loads per thread and step
-    uint32_t sv = 0;
-    int page[2], nv[2];
-    uint4 r[NL];
-    uint16_t ks, vs;
-    auto fetch = [&](int i) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int w = 2 * (i0 + i) + x;
-        page[x] = w < p.pages ? p.ptable[w] : 0;
-        nv[x] = w < p.pages ? min(64, p.prefix - 64 * w) : 0;
-        if (page[x] < 0 || page[x] >= p.q8.n_pages) {
-          set_error(kErrBadIndex);
-          page[x] = nv[x] = 0;
-        }
+    const int kt = tid - 128;
+    constexpr int NL = D / 32;                       // 16-byte loads per thread and page
+    constexpr int CPR = D / 16;                      // 16-byte pieces of a row
+    const int ch = kt % CPR, rw0 = kt / CPR;         // load x is row rw0 + x (128 / CPR): same row mod 8
+    // pieces 2 c and 2 c + 1 of the FP16 row; lanes 4-7 store the odd one first, so
+    // that eight lanes meet the eight 16-byte columns
+    const int odd = (ch >> 2) & 1, c0 = (ch & 3) * 2 + odd, c1 = (ch & 3) * 2 + 1 - odd;
+    const uint32_t at = (ch >> 2) * 64 * 128 + rw0 * 128;
+    const uint32_t d0 = at + ((c0 ^ (rw0 & 7)) << 4), d1 = at + ((c1 ^ (rw0 & 7)) << 4);
+    struct Buf {
+      uint4 r[NL];
+      uint16_t ks, vs;
+      int nv;
+    } buf[2];
+    uint32_t svm = 0;
+    auto fetch = [&](int j, Buf &d) {
+      const int w = j0 + j;
+      int page = p.ptable[w];
+      d.nv = min(64, p.prefix - 64 * w);
+      if (page < 0 || page >= p.q8.n_pages) {
+        set_error(kErrBadIndex);
+        page = d.nv = 0;
       }
+      const size_t ph = (size_t)page * H + h;
 #pragma unroll
-      for (int x = 0; x < NL; ++x) {
-        const size_t ph = (size_t)page[x >= NL / 2] * H + h;
-        r[x] = q8_ldg(p.q8.k + ph * 64 * D + (size_t)(kt + 128 * (x % (NL / 2))) * 16);
-      }
-      const size_t ph = (size_t)page[kt >> 6] * H + h;
-      ks = p.q8.ks[ph * 64 + (kt & 63)];
-      vs = p.q8.vs[ph * 64 + (kt & 63)];
+      for (int x = 0; x < NL; ++x) d.r[x] = q8_ldg(p.q8.k + ph * 64 * D + (size_t)(kt + 128 * x) * 16);
+      d.ks = p.q8.ks[ph * 64 + (kt & 63)];
+      d.vs = p.q8.vs[ph * 64 + (kt & 63)];
     };
-    if (n > 0) fetch(0);
-    for (int i = 0; i < n && ok; ++i) {
-      const int slot = i % NK, sb = i & 1;
-      if (i >= NK && !mbar_wait(&k_empty[slot], ((i / NK) - 1) & 1)) { ok = false; break; }
-      uint8_t *dst = pfx_sm + L::k + slot * DB * L::kTile;
+    auto put = [&](int j, Buf &d) {
+      const int slot = j % NK, sb = j & 3;
+      if (j >= NK && !mbar_wait(&k_empty[slot], ((j / NK) - 1) & 1)) return false;
+      uint8_t *dst = pfx_sm + L::k + slot * L::kPage;
 #pragma unroll
       for (int x = 0; x < NL; ++x) {
-        const int at = kt + 128 * (x % (NL / 2)), rw = at / NL + (x >= NL / 2 ? 64 : 0), ch = at % NL;
         uint4 lo, hi;
-        pfx_f16(r[x], lo, hi);
-        // chunks 2 c and 2 c + 1 of row rw; lanes 4-7 store the odd one first, so that
-        // eight lanes meet the eight chunk columns
-        const int c = (ch & 3) * 2, odd = (ch >> 2) & 1;
-        uint8_t *base = dst + (ch >> 2) * L::kTile + rw * 128;
-        *reinterpret_cast<uint4 *>(base + (((c + odd) ^ (rw & 7)) << 4)) = odd ? hi : lo;
-        *reinterpret_cast<uint4 *>(base + (((c + 1 - odd) ^ (rw & 7)) << 4)) = odd ? lo : hi;
+        pfx_f16(d.r[x], lo, hi);
+        const int o = x * (128 / CPR) * 128;
+        *reinterpret_cast<uint4 *>(dst + d0 + o) = odd ? hi : lo;
+        *reinterpret_cast<uint4 *>(dst + d1 + o) = odd ? lo : hi;
       }
-      // the weights of step i - 2 are done with this slot of scales
-      if (i >= 2 && !mbar_wait(&s_empty[sb], ((i >> 1) - 1) & 1)) { ok = false; break; }
-      const bool alive = (kt & 63) < nv[kt >> 6];
-      sc[sb][kt] = make_float2(bf16_bits_to_f32(ks), bf16_bits_to_f32(vs));
-      if (alive && vs < 0x7F80u) sv = max(sv, (uint32_t)vs);
-      if ((kt & 63) == 0) s_nv[sb][kt >> 6] = nv[kt >> 6];
+      // the weights of page j - 4 are done with this slot of scales
+      if (j >= 4 && !mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1)) return false;
+      const bool alive = (kt & 63) < d.nv;
+      if (alive && d.vs < 0x7F80u) svm = max(svm, (uint32_t)d.vs);
+      const bool nan = __any_sync(0xffffffffu, d.vs >= 0x7F80u);
+      if (kt < 64) {
+        s_a[sb][kt] = bf16_bits_to_f32(d.ks);
+        s_v[sb][kt] = bf16_bits_to_f32(d.vs);
+      }
+      if (kt == 0) s_nv[sb][0] = d.nv;
+      if (kt == 0 || kt == 32) reinterpret_cast<uint16_t *>(&s_nv[sb][1])[kt >> 5] = nan;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&k_full[slot]);
         mbar_arrive(&sc_full[sb]);
       }
-      if (i + 1 < n) fetch(i + 1);
+      return true;
+    };
+    fetch(0, buf[0]);
+    if (n > 1) fetch(1, buf[1]);
+    for (int j = 0; j < n && ok; j += 2) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (j + u >= n) break;
+        if (!put(j + u, buf[u])) { ok = false; break; }
+        if (j + u + 2 < n) fetch(j + u + 2, buf[u]);
+      }
     }
     if constexpr (!PV) {
       pdl_wait();                                    // svmax was cleared by q8_logits
-      sv = __reduce_max_sync(0xffffffffu, sv);
-      if (lane == 0 && sv != 0) atomicMax(&p.svmax[h], sv << 16);
+      __syncwarp();
+      svm = __reduce_max_sync(0xffffffffu, svm);
+      if (lane == 0 && svm != 0) atomicMax(&p.svmax[h], svm << 16);
     }
-  } else if (warp < 16) {
+  } else if (warp < 12) {
     // ------------------------------------ V ------------------------------------
     if constexpr (PV) {
-      const int vt = tid - 384;
-      constexpr int NL = D / 32;
-      uint4 r[NL];
-      auto fetch = [&](int j) {                      // j = 2 (step) + page of the step
-        const int w = 2 * i0 + j;
-        int page = w < p.pages ? p.ptable[w] : 0;
-        if (page < 0 || page >= p.q8.n_pages) page = 0;
+      const int vt = tid - 256;
+      constexpr int NL = D / 32;                     // load x is row vt / 4 + 32 x
+      const int rw0 = vt >> 2, c0 = (vt & 3) * 2;
+      const uint32_t d0 = rw0 * 128 + ((c0 ^ (rw0 & 7)) << 4), d1 = rw0 * 128 + (((c0 + 1) ^ (rw0 & 7)) << 4);
+      uint4 buf[2][NL];
+      auto fetch = [&](int j, uint4 *r) {
+        int page = p.ptable[j0 + j];
+        if (page < 0 || page >= p.q8.n_pages) page = 0;   // its keys weigh nothing
         const int8_t *src = p.q8.v + ((size_t)page * H + h) * 64 * D + vt * 16;
 #pragma unroll
         for (int x = 0; x < NL; ++x) r[x] = q8_ldg(src + x * 2048);
       };
-      if (n > 0) fetch(0);
-      for (int j = 0; j < 2 * n && ok; ++j) {
+      auto put = [&](int j, const uint4 *r) {
         const int slot = j & 1;
-        if (j >= 2 && !mbar_wait(&v_empty[slot], ((j >> 1) - 1) & 1)) { ok = false; break; }
+        if (j >= 2 && !mbar_wait(&v_empty[slot], ((j >> 1) - 1) & 1)) return false;
         uint8_t *dst = pfx_sm + L::v + slot * L::kV;
 #pragma unroll
         for (int x = 0; x < NL; ++x) {
-          const int at = vt + 128 * x, rw = at >> 2, c = (at & 3) * 2;
           uint4 lo, hi;
           pfx_f16(r[x], lo, hi);
-          *reinterpret_cast<uint4 *>(dst + rw * 128 + ((c ^ (rw & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4 *>(dst + rw * 128 + (((c + 1) ^ (rw & 7)) << 4)) = hi;
+          *reinterpret_cast<uint4 *>(dst + d0 + x * 32 * 128) = lo;
+          *reinterpret_cast<uint4 *>(dst + d1 + x * 32 * 128) = hi;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[slot]);
-        if (j + 1 < 2 * n) fetch(j + 1);
+        return true;
+      };
+      fetch(0, buf[0]);
+      if (n > 1) fetch(1, buf[1]);
+      for (int j = 0; j < n && ok; j += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (j + u >= n) break;
+          if (!put(j + u, buf[u])) { ok = false; break; }
+          if (j + u + 2 < n) fetch(j + u + 2, buf[u]);
+        }
       }
     }
   } else if (lane == 0) {
     // ------------------------------- MMA issuer -------------------------------
-    constexpr uint32_t id_s = umma_idesc_f16(128, 128), id_o = umma_idesc_f16(128, D);
+    constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_o = umma_idesc_f16(128, D);
     const uint32_t q0 = smem_u32(pfx_sm + L::q), k0 = smem_u32(pfx_sm + L::k);
     const uint32_t v0 = smem_u32(pfx_sm + L::v), w0 = smem_u32(pfx_sm + L::w);
-    auto weights_v = [&](int i) {
-      if (!mbar_wait(w_full, i & 1)) return false;
+    auto weights_v = [&](int j) {
+      const int slot = j & 1;
+      if (!mbar_wait(&w_full[slot], (j >> 1) & 1) || !mbar_wait(&v_full[slot], (j >> 1) & 1)) return false;
+      tc_fence_after();
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!mbar_wait(&v_full[x], i & 1)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma_f16(tmem, umma_desc_sw128(w0 + x * L::kTile + 32 * k),
-                     umma_desc_sw128(v0 + x * L::kV + 32 * k), id_o, i > 0 || x > 0 || k > 0);
-        tc_commit(&v_empty[x]);
-      }
-      tc_commit(w_empty);
+      for (int k = 0; k < 4; ++k)
+        tc_mma_f16(tmem, umma_desc_sw128(w0 + slot * L::kTile + 32 * k),
+                   umma_desc_sw128(v0 + slot * L::kV + 32 * k), id_o, j > 0 || k > 0);
+      tc_commit(&v_empty[slot]);                     // frees the slot's V and weights
       return true;
     };
-    for (int i = 0; i < n && ok; ++i) {
-      const int slot = i % NK, sb = i & 1;
-      if (!mbar_wait(&k_full[slot], (i / NK) & 1)) { ok = false; break; }
-      if (i >= 2 && !mbar_wait(&s_empty[sb], ((i >> 1) - 1) & 1)) { ok = false; break; }
+    for (int j = 0; j < n && ok; ++j) {
+      const int slot = j % NK, sb = j & 3;
+      if (!mbar_wait(&k_full[slot], (j / NK) & 1)) { ok = false; break; }
+      if (j >= 4 && !mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1)) { ok = false; break; }
       tc_fence_after();
-      const uint32_t acc = tmem + (PV ? 256 : 0) + 128 * sb, kb = k0 + slot * DB * L::kTile;
+      const uint32_t acc = tmem + (PV ? 256 : 0) + 64 * sb, kb = k0 + slot * L::kPage;
 #pragma unroll
-      for (int j = 0; j < DB; ++j)
+      for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma_f16(acc, umma_desc_sw128(q0 + j * L::kTile + 32 * k),
-                     umma_desc_sw128(kb + j * L::kTile + 32 * k), id_s, j > 0 || k > 0);
+          tc_mma_f16(acc, umma_desc_sw128(q0 + i * L::kTile + 32 * k),
+                     umma_desc_sw128(kb + i * 64 * 128 + 32 * k), id_s, i > 0 || k > 0);
       tc_commit(&k_empty[slot]);
       tc_commit(&s_full[sb]);
       if constexpr (PV)
-        if (i > 0 && !weights_v(i - 1)) { ok = false; break; }
+        if (j >= kPfxAhead && !weights_v(j - kPfxAhead)) { ok = false; break; }
     }
     if constexpr (PV) {
-      if (ok && n > 0) ok = weights_v(n - 1);
+      for (int j = max(0, n - kPfxAhead); j < n && ok; ++j) ok = weights_v(j);
       tc_commit(o_full);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, PV ? 512 : 256);
   }
@@ -447,17 +518,16 @@ namespace {
 struct PfxLayout {
   Q8Layout q8;
   size_t mrow, svmax, po, pl, total;
-  int pages, steps, splits, rows, row_tiles;
+  int pages, splits, rows, row_tiles;
 };
 PfxLayout pfx_layout(const Q8Shape &s) {
   PfxLayout y{};
   y.q8 = q8_layout(s);
   y.pages = (s.prefix + 63) / 64;
-  y.steps = (y.pages + 1) / 2;
   y.rows = s.B * (s.Hq / s.Hkv);
   y.row_tiles = (y.rows + 127) / 128;
   // one CTA per SM: the splits that fill one round of the SMs
-  y.splits = std::max(1, std::min(y.steps, kQ8Sms / (y.row_tiles * s.Hkv)));
+  y.splits = std::max(1, std::min(y.pages, kQ8Sms / (y.row_tiles * s.Hkv)));
   size_t at = y.q8.total;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -514,7 +584,7 @@ cudaError_t launch_prefix_attention(const Q8Args &a, cudaStream_t st, Launcher &
   PfxParams p{};
   p.q8 = q8_params(a, y.q8);
   p.ptable = a.ptable;
-  p.prefix = a.s.prefix; p.pages = y.pages; p.steps = y.steps; p.splits = y.splits; p.rows = y.rows;
+  p.prefix = a.s.prefix; p.pages = y.pages; p.splits = y.splits; p.rows = y.rows;
   p.mrow = reinterpret_cast<uint32_t *>(ws + y.mrow);
   p.svmax = reinterpret_cast<uint32_t *>(ws + y.svmax);
   p.po = reinterpret_cast<float *>(ws + y.po);
