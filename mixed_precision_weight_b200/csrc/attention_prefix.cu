@@ -11,12 +11,15 @@
 // and q8_merge adds the items' and the splits' partials in order.
 //
 // A CTA holds 128 rows of Q and walks a split of the prefix page by page (64
-// keys).  Warps 0-3 turn S into weights (a thread per row), warps 4-7 bring K
-// and warps 8-11 V from global memory through registers, two pages ahead, where
-// the 8-bit codes become FP16, into 128-byte-swizzled shared memory, and one
-// thread of warp 12 issues the MMAs.  Four S buffers in tensor memory; Q K^T of
-// page j is issued before w V of page j - 2, so that a page's weights are formed
-// behind two products.
+// keys).  Warps 0-7 turn S into weights (a warpgroup per page, alternating, a
+// thread per row); warps 8-19 bring pages from global memory through registers,
+// where the 8-bit codes become FP16, into a ring of 128-byte-swizzled shared
+// memory (a warpgroup per page, in the order the products take them); one thread
+// of warp 20 issues the MMAs.  Q lies in tensor memory and the weights overwrite
+// their S there, so that both products read one operand only from shared memory:
+// with Q there too, a 128 x 64 x 16 product took 66 cycles instead of 32, its
+// operands' bytes at 128 per cycle.  Q K^T of page j + 1 is issued before w V of
+// page j.
 //
 // Number formats: a code is exact in FP16 (1024 + u from a byte permutation,
 // minus 1152), and so is a query scaled by a power of two to 2^14 .. 2^15 (BF16
@@ -29,8 +32,9 @@
 
 namespace dvssq {
 
-constexpr int kPfxThreads = 13 * 32;
-constexpr int kPfxAhead = 2;             // pages of Q K^T issued ahead of w V
+constexpr int kPfxThreads = 6 * 128;     // two weight, three loading and one issuing warpgroup
+constexpr int kPfxLoaders = 3;
+constexpr int kPfxRing = 6;              // pages of FP16 codes in shared memory
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct PfxParams {
@@ -69,6 +73,41 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t r[32]) {
   asm volatile("" : "+r"(r[30]), "+r"(r[31]) : : "memory");
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      :
+      : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16 (A: two FP16 per 32-bit column)
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 16 codes -> 16 FP16 values in order, as two 16-byte chunks
 __device__ __forceinline__ void pfx_f16(const uint4 &c, uint4 &lo, uint4 &hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -96,37 +135,35 @@ __device__ __forceinline__ float ex2_approx(float x) {
 template <int D, bool PV>
 struct PfxSmem {
   static constexpr int DB = D / 64;
-  static constexpr int NK = !PV || D < 256 ? 4 : 2;      // K slots (a page each)
-  static constexpr int kPage = DB * 64 * 128;            // FP16 K page: DB blocks of 64 rows x 128 bytes
-  static constexpr int kTile = 128 * 128;                // 128 rows of 128 bytes
-  static constexpr int kV = D * 128;                     // FP16 V page: D rows of 128 bytes
-  static constexpr int q = 0;
-  static constexpr int k = q + DB * kTile;
-  static constexpr int v = k + NK * kPage;
-  static constexpr int w = v + (PV ? 2 * kV : 0);
-  static constexpr int sa = w + (PV ? 2 * kTile : 0);    // float [4][64]: key scales
+  static constexpr int kSlot = D * 128;                  // a page: K [DB][64 rows][128 B] or V [D rows][128 B]
+  static constexpr int kQRow = 2 * D + 16;               // a staged row of Q (in the ring, before it fills)
+  static constexpr int sa = kPfxRing * kSlot;            // float [4][64]: key scales
   static constexpr int sv = sa + 4 * 64 * 4;             // float [4][64]: value scales
   static constexpr int step = sv + 4 * 64 * 4;           // float [128]
   static constexpr int nv = step + 128 * 4;              // int [4][2]: live keys, NaN value scales
   static constexpr int bar = nv + 32;
-  static constexpr int bytes = bar + 27 * 8 + 16;
+  static constexpr int bytes = bar + (2 * kPfxRing + 15) * 8 + 16;
+  static_assert(128 * kQRow <= kPfxRing * kSlot && 8 * 32 * 36 * 4 <= kPfxRing * kSlot, "staging fits the ring");
+  // tensor memory columns: O, then Q, then the S buffers (64 columns each)
+  static constexpr int NS = PV ? 2 : 4;
+  static constexpr int tq = PV ? 256 : 0;
+  static constexpr int ts = tq + 128;
 };
 
 template <int D, bool PV>
 __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) {
   using L = PfxSmem<D, PV>;
-  constexpr int DB = L::DB, NK = L::NK, VPL = D / 32;
+  constexpr int DB = L::DB, VPL = D / 32, NS = L::NS, R = kPfxRing;
   extern __shared__ __align__(1024) uint8_t pfx_sm[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(pfx_sm + L::bar);
-  uint64_t *k_full = bar, *k_empty = bar + 4, *s_full = bar + 8, *s_empty = bar + 12,
-           *sc_full = bar + 16, *v_full = bar + 20, *v_empty = bar + 22, *w_full = bar + 24,
-           *o_full = bar + 26;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 27);
+  uint64_t *full = bar, *empty = bar + R, *s_full = bar + 2 * R, *s_empty = s_full + 4,
+           *sc_full = s_empty + 4, *w_full = sc_full + 4, *o_full = w_full + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 1);
   float (*s_a)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sa);
   float (*s_v)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sv);
   float *s_step = reinterpret_cast<float *>(pfx_sm + L::step);
   int (*s_nv)[2] = reinterpret_cast<int (*)[2]>(pfx_sm + L::nv);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
   const int split = blockIdx.x, h = blockIdx.y, rt = blockIdx.z;
   const int H = p.q8.H, G = p.q8.G;
   const int j0 = (int)((long long)p.pages * split / p.splits);
@@ -136,33 +173,32 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     return;
   }
   if (tid == 0) {
+    for (int s = 0; s < R; ++s) {
+      mbar_init(&full[s], 4);
+      mbar_init(&empty[s], 1);
+    }
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&k_full[s], 4);
-      mbar_init(&k_empty[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&s_empty[s], 4);
       mbar_init(&sc_full[s], 4);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&v_full[s], 4);
-      mbar_init(&v_empty[s], 1);
-      mbar_init(&w_full[s], 4);
-    }
+    mbar_init(&w_full[0], 4);
+    mbar_init(&w_full[1], 4);
     mbar_init(o_full, 1);
     fence_mbarrier_init();
   }
-  if (warp == 12) {
-    tmem_alloc(tmem_slot, PV ? 512 : 256);
+  if (warp == 20) {
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  // Q: a warp per row, five rows in flight; row r of the tile is query head
-  // h G + r % G of sequence r / G
-#pragma unroll 1
-  for (int r0 = warp; r0 < 128; r0 += 5 * 13) {
-    KvRaw<VPL> raw[5];
+  // Q: a warp per row, all its rows in flight; row r of the tile is query head
+  // h G + r % G of sequence r / G.  Staged as FP16 rows, then into tensor memory.
+  {
+    constexpr int NR = 6;                    // 24 warps, 128 rows
+    KvRaw<VPL> raw[NR];
 #pragma unroll
-    for (int u = 0; u < 5; ++u) {
-      const int r = r0 + 13 * u, rr = rt * 128 + r;
+    for (int u = 0; u < NR; ++u) {
+      const int r = warp + 24 * u, rr = rt * 128 + r;
 #pragma unroll
       for (int i = 0; i < VPL / 2; ++i) raw[u].w[i] = 0;
       if (r < 128 && rr < p.rows) {
@@ -171,8 +207,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     }
 #pragma unroll
-    for (int u = 0; u < 5; ++u) {
-      const int r = r0 + 13 * u;
+    for (int u = 0; u < NR; ++u) {
+      const int r = warp + 24 * u;
       if (r >= 128) break;
       uint32_t m = 0;
 #pragma unroll
@@ -182,8 +218,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       // times 2^(14 - e) in two exact steps (14 - e is 140 at most)
       const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100);
       const float f0 = __int_as_float((up + 127) << 23), f1 = __int_as_float((14 - e - up + 127) << 23);
-      const int dim = lane * VPL, kb = dim >> 6, c = (dim & 63) >> 3;
-      uint8_t *dst = pfx_sm + L::q + kb * L::kTile + r * 128 + ((c ^ (r & 7)) << 4) + 2 * (dim & 7);
+      uint8_t *dst = pfx_sm + r * L::kQRow + 2 * lane * VPL;
 #pragma unroll
       for (int i = 0; i < VPL / 2; ++i) {
         const __half2 x = __floats2half2_rn(bf16_bits_to_f32(raw[u].w[i] & 0xFFFFu) * f0 * f1,
@@ -193,7 +228,6 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       if (lane == 0) s_step[r] = finite ? ldexpf(1.0f, e - 14) : __uint_as_float(0x7FC00000u);
     }
   }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -201,14 +235,31 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
-
   if (warp < 4) {
+#pragma unroll
+    for (int j = 0; j < DB; ++j) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(pfx_sm + tid * L::kQRow + 128 * j + 16 * i);
+        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+      }
+      tmem_st32(tmem + ((uint32_t)(32 * warp) << 16) + L::tq + 32 * j, w);
+    }
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  if (wg < 2) {
     // ------------------------------- weights -------------------------------
-    const int row = tid, rr = rt * 128 + row;
+    reg_inc<112>();
+    const int row = tid & 127, rr = rt * 128 + row;
     const bool live = rr < p.rows;
     const int b = live ? rr / G : 0, hq = h * G + (live ? rr - b * G : 0);
     const float r1 = s_step[row] * p.q8.scale;       // logit = S ks r1
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float mx = -INFINITY, x0 = 0.f, floor2 = -INFINITY;
     float2 sum = make_float2(0.f, 0.f);
     int shift = 0;
@@ -231,17 +282,15 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     }
     const float r2 = r1 * kLog2e;
-    for (int j = 0; j < n && ok; ++j) {
-      const int sb = j & 3, par = (j >> 2) & 1;
-      bool got = mbar_wait(&sc_full[sb], par) && mbar_wait(&s_full[sb], par);
-      if constexpr (PV)
-        if (j >= 2) got = got && mbar_wait(&v_empty[j & 1], ((j >> 1) - 1) & 1);   // the slot's w V is done
+    for (int j = wg; j < n && ok; j += 2) {
+      const int sb = j & 3, ss = j % NS;
+      const bool got = mbar_wait(&sc_full[sb], (j >> 2) & 1) && mbar_wait(&s_full[ss], (j / NS) & 1);
       // a warp gives up as one: the tensor-memory loads are warp-wide
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
       const int nv = s_nv[sb][0];
       const bool plain = nv == 64 && (s_nv[sb][1] == 0);
-      const uint32_t src = lane_base + (PV ? 256 : 0) + 64 * sb;
+      const uint32_t src = lane_base + L::ts + 64 * ss;
       uint32_t s[64];
       tmem_ld32(src, s);
       tmem_ld32(src + 32, s + 32);
@@ -263,54 +312,50 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
           }
         }
       } else {
-        uint8_t *dst = pfx_sm + L::w + (j & 1) * L::kTile + row * 128;
         const float2 rr2 = make_float2(r2, r2), xx0 = make_float2(x0, x0);
+        uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 64; i += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int t = 0; t < 8; t += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(&s_a[sb][i + t]);
-            const float4 v = *reinterpret_cast<const float4 *>(&s_v[sb][i + t]);
-            const float2 x = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + t]), __uint_as_float(s[i + t + 1])),
-                                               make_float2(a.x, a.y)), rr2, xx0);
-            const float2 y = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + t + 2]), __uint_as_float(s[i + t + 3])),
-                                               make_float2(a.z, a.w)), rr2, xx0);
-            float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            float2 ey = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            float2 wx, wy;
-            // a NaN logit is kept
-            if (x.x < floor2) ex.x = 0.f;
-            if (x.y < floor2) ex.y = 0.f;
-            if (y.x < floor2) ey.x = 0.f;
-            if (y.y < floor2) ey.y = 0.f;
-            if (plain) {
-              wx = mat_mul2(ex, make_float2(v.x, v.y));
-              wy = mat_mul2(ey, make_float2(v.z, v.w));
-            } else {
-              // keys past the prefix's end weigh nothing, and the value scale of a key
-              // without weight is not looked at
-              if (i + t >= nv) ex.x = 0.f;
-              if (i + t + 1 >= nv) ex.y = 0.f;
-              if (i + t + 2 >= nv) ey.x = 0.f;
-              if (i + t + 3 >= nv) ey.y = 0.f;
-              wx = make_float2(ex.x == 0.f ? 0.f : ex.x * v.x, ex.y == 0.f ? 0.f : ex.y * v.y);
-              wy = make_float2(ey.x == 0.f ? 0.f : ey.x * v.z, ey.y == 0.f ? 0.f : ey.y * v.w);
-            }
-            sum = mat_add2(sum, mat_add2(ex, ey));
-            const __half2 ox = __floats2half2_rn(wx.x, wx.y), oy = __floats2half2_rn(wy.x, wy.y);
-            w[t / 2] = *reinterpret_cast<const uint32_t *>(&ox);
-            w[t / 2 + 1] = *reinterpret_cast<const uint32_t *>(&oy);
+        for (int i = 0; i < 64; i += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(&s_a[sb][i]);
+          const float4 v = *reinterpret_cast<const float4 *>(&s_v[sb][i]);
+          const float2 x = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                             make_float2(a.x, a.y)), rr2, xx0);
+          const float2 y = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])),
+                                             make_float2(a.z, a.w)), rr2, xx0);
+          float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          float2 ey = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          float2 wx, wy;
+          // below the haze threshold: dropped (a NaN logit is kept)
+          if (x.x < floor2) ex.x = 0.f;
+          if (x.y < floor2) ex.y = 0.f;
+          if (y.x < floor2) ey.x = 0.f;
+          if (y.y < floor2) ey.y = 0.f;
+          if (plain) {
+            wx = mat_mul2(ex, make_float2(v.x, v.y));
+            wy = mat_mul2(ey, make_float2(v.z, v.w));
+          } else {
+            // keys past the prefix's end weigh nothing, and the value scale of a key
+            // without weight is not looked at
+            if (i >= nv) ex.x = 0.f;
+            if (i + 1 >= nv) ex.y = 0.f;
+            if (i + 2 >= nv) ey.x = 0.f;
+            if (i + 3 >= nv) ey.y = 0.f;
+            wx = make_float2(ex.x == 0.f ? 0.f : ex.x * v.x, ex.y == 0.f ? 0.f : ex.y * v.y);
+            wy = make_float2(ey.x == 0.f ? 0.f : ey.x * v.z, ey.y == 0.f ? 0.f : ey.y * v.w);
           }
-          *reinterpret_cast<uint4 *>(dst + (((i >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          sum = mat_add2(sum, mat_add2(ex, ey));
+          const __half2 ox = __floats2half2_rn(wx.x, wx.y), oy = __floats2half2_rn(wy.x, wy.y);
+          w[i / 2] = *reinterpret_cast<const uint32_t *>(&ox);
+          w[i / 2 + 1] = *reinterpret_cast<const uint32_t *>(&oy);
         }
-        fence_proxy_async_smem();
+        tmem_st32(src, w);                           // over this row's S
+        tmem_st_wait();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&s_empty[sb]);
-        if constexpr (PV) mbar_arrive(&w_full[j & 1]);
+        if constexpr (PV) mbar_arrive(&w_full[ss]);
       }
     }
     if constexpr (!PV) {
@@ -322,14 +367,20 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       tc_fence_after();
       const float back = ldexpf(1.0f, -shift);
       const size_t at = ((size_t)split * H + h) * p.rows;
-      if (live) p.pl[at + rr] = (sum.x + sum.y) * back;
-      // 32 x 32 blocks through shared memory (K's, free now): whole 128-byte lines out
-      float (*st)[36] = reinterpret_cast<float (*)[36]>(pfx_sm + L::k + warp * 32 * 36 * 4);
+      // the two warpgroups' sums of the row (every thread has read its step by now:
+      // the last weights were waited for)
+      if (wg == 1) s_step[row] = sum.x + sum.y;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (wg == 0 && live) p.pl[at + rr] = (sum.x + sum.y + s_step[row]) * back;
+      // each warpgroup half of the columns, 32 x 32 blocks through shared memory (the
+      // ring, free now): whole 128-byte lines out
+      float (*st)[36] = reinterpret_cast<float (*)[36]>(pfx_sm + warp * 32 * 36 * 4);
       const int sub = lane >> 3, c4 = (lane & 7) * 4;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
+      for (int cc = 0; cc < D / 64; ++cc) {
+        const int col = wg * (D / 2) + 32 * cc;
         uint32_t o[32];
-        tmem_ld32(lane_base + 32 * cc, o);
+        tmem_ld32(lane_base + col, o);
         tmem_ld_wait32(o);
         __syncwarp();
 #pragma unroll
@@ -340,84 +391,97 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int rw = 4 * i + sub, gr = rt * 128 + 32 * warp + rw;
+          const int rw = 4 * i + sub, gr = rt * 128 + 32 * (warp & 3) + rw;
           if (gr < p.rows && ok)
-            *reinterpret_cast<float4 *>(p.po + (at + gr) * D + 32 * cc + c4) =
+            *reinterpret_cast<float4 *>(p.po + (at + gr) * D + col + c4) =
                 *reinterpret_cast<const float4 *>(&st[rw][c4]);
         }
       }
-      tc_fence_before();
     }
-  } else if (warp < 8) {
-    // -------------------------------- K and scales --------------------------------
-    const int kt = tid - 128;
+    tc_fence_before();
+  } else if (wg < 2 + kPfxLoaders) {
+    // ------------------------- pages into the ring -------------------------
+    reg_dec<72>();
+    const int kt = tid & 127, jobs = PV ? 2 * n : n;
     constexpr int NL = D / 32;                       // 16-byte loads per thread and page
-    constexpr int CPR = D / 16;                      // 16-byte pieces of a row
-    const int ch = kt % CPR, rw0 = kt / CPR;         // load x is row rw0 + x (128 / CPR): same row mod 8
-    // pieces 2 c and 2 c + 1 of the FP16 row; lanes 4-7 store the odd one first, so
-    // that eight lanes meet the eight 16-byte columns
-    const int odd = (ch >> 2) & 1, c0 = (ch & 3) * 2 + odd, c1 = (ch & 3) * 2 + 1 - odd;
-    const uint32_t at = (ch >> 2) * 64 * 128 + rw0 * 128;
-    const uint32_t d0 = at + ((c0 ^ (rw0 & 7)) << 4), d1 = at + ((c1 ^ (rw0 & 7)) << 4);
-    struct Buf {
-      uint4 r[NL];
-      uint16_t ks, vs;
-      int nv;
-    } buf[2];
+    constexpr int CPR = D / 16;                      // 16-byte pieces of a K row
+    // K piece: load x is row kr + x (128 / CPR), piece ch; FP16 pieces 2 c and 2 c + 1 of
+    // the row; lanes 4-7 store the odd one first, so that eight lanes meet the
+    // eight 16-byte columns
+    const int ch = kt % CPR, kr = kt / CPR, odd = (ch >> 2) & 1;
+    const uint32_t kat = (ch >> 2) * 64 * 128 + kr * 128;
+    const uint32_t k0 = kat + ((((ch & 3) * 2 + odd) ^ (kr & 7)) << 4);
+    const uint32_t k1 = kat + ((((ch & 3) * 2 + 1 - odd) ^ (kr & 7)) << 4);
+    // V piece: load x is row kt / 4 + 32 x
+    const int vr = kt >> 2;
+    const uint32_t v0 = vr * 128 + ((((kt & 3) * 2) ^ (vr & 7)) << 4);
+    const uint32_t v1 = vr * 128 + ((((kt & 3) * 2 + 1) ^ (vr & 7)) << 4);
+    // jobs in the order of the products: K(0), then K(j + 1), V(j), .., V(n - 1)
+    auto is_k = [&](int t) { return !PV || t == 0 || ((t & 1) && t < 2 * n - 1); };
+    auto page_of = [&](int t) { return !PV ? t : t == 2 * n - 1 ? n - 1 : is_k(t) ? (t + 1) >> 1 : (t >> 1) - 1; };
+    uint4 r[NL];
+    uint16_t ks = 0, vs = 0;
+    int nv = 0;
     uint32_t svm = 0;
-    auto fetch = [&](int j, Buf &d) {
-      const int w = j0 + j;
+    auto fetch = [&](int t) {
+      const int w = j0 + page_of(t);
+      const bool k = is_k(t);
       int page = p.ptable[w];
-      d.nv = min(64, p.prefix - 64 * w);
-      if (page < 0 || page >= p.q8.n_pages) {
+      nv = min(64, p.prefix - 64 * w);
+      if (page < 0 || page >= p.q8.n_pages) {        // its keys weigh nothing
         set_error(kErrBadIndex);
-        page = d.nv = 0;
+        page = nv = 0;
       }
       const size_t ph = (size_t)page * H + h;
+      const int8_t *src = (k ? p.q8.k : p.q8.v) + ph * 64 * D + kt * 16;
 #pragma unroll
-      for (int x = 0; x < NL; ++x) d.r[x] = q8_ldg(p.q8.k + ph * 64 * D + (size_t)(kt + 128 * x) * 16);
-      d.ks = p.q8.ks[ph * 64 + (kt & 63)];
-      d.vs = p.q8.vs[ph * 64 + (kt & 63)];
+      for (int x = 0; x < NL; ++x) r[x] = q8_ldg(src + x * 2048);
+      if (k) {
+        ks = p.q8.ks[ph * 64 + (kt & 63)];
+        vs = p.q8.vs[ph * 64 + (kt & 63)];
+      }
     };
-    auto put = [&](int j, Buf &d) {
-      const int slot = j % NK, sb = j & 3;
-      if (j >= NK && !mbar_wait(&k_empty[slot], ((j / NK) - 1) & 1)) return false;
-      uint8_t *dst = pfx_sm + L::k + slot * L::kPage;
+    int t = wg - 2;
+    if (t < jobs) fetch(t);
+    for (; t < jobs && ok; t += kPfxLoaders) {
+      const int slot = t % R, j = page_of(t), sb = j & 3;
+      if (t >= R && !mbar_wait(&empty[slot], ((t / R) - 1) & 1)) { ok = false; break; }
+      uint8_t *dst = pfx_sm + slot * L::kSlot;
+      const bool k = is_k(t);
+      if (k) {
 #pragma unroll
-      for (int x = 0; x < NL; ++x) {
-        uint4 lo, hi;
-        pfx_f16(d.r[x], lo, hi);
-        const int o = x * (128 / CPR) * 128;
-        *reinterpret_cast<uint4 *>(dst + d0 + o) = odd ? hi : lo;
-        *reinterpret_cast<uint4 *>(dst + d1 + o) = odd ? lo : hi;
+        for (int x = 0; x < NL; ++x) {
+          uint4 lo, hi;
+          pfx_f16(r[x], lo, hi);
+          const int o = x * (128 / CPR) * 128;
+          *reinterpret_cast<uint4 *>(dst + k0 + o) = odd ? hi : lo;
+          *reinterpret_cast<uint4 *>(dst + k1 + o) = odd ? lo : hi;
+        }
+        // the weights of page j - 4 are done with this slot of scales
+        if (j >= 4 && !mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1)) { ok = false; break; }
+        if ((kt & 63) < nv && vs < 0x7F80u) svm = max(svm, (uint32_t)vs);
+        const bool nan = __any_sync(0xffffffffu, vs >= 0x7F80u);
+        if (kt < 64) {
+          s_a[sb][kt] = bf16_bits_to_f32(ks);
+          s_v[sb][kt] = bf16_bits_to_f32(vs);
+        }
+        if (kt == 0) s_nv[sb][0] = nv;
+        if (kt == 0 || kt == 32) reinterpret_cast<uint16_t *>(&s_nv[sb][1])[kt >> 5] = nan;
+      } else {
+#pragma unroll
+        for (int x = 0; x < NL; ++x) {
+          uint4 lo, hi;
+          pfx_f16(r[x], lo, hi);
+          *reinterpret_cast<uint4 *>(dst + v0 + x * 32 * 128) = lo;
+          *reinterpret_cast<uint4 *>(dst + v1 + x * 32 * 128) = hi;
+        }
       }
-      // the weights of page j - 4 are done with this slot of scales
-      if (j >= 4 && !mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1)) return false;
-      const bool alive = (kt & 63) < d.nv;
-      if (alive && d.vs < 0x7F80u) svm = max(svm, (uint32_t)d.vs);
-      const bool nan = __any_sync(0xffffffffu, d.vs >= 0x7F80u);
-      if (kt < 64) {
-        s_a[sb][kt] = bf16_bits_to_f32(d.ks);
-        s_v[sb][kt] = bf16_bits_to_f32(d.vs);
-      }
-      if (kt == 0) s_nv[sb][0] = d.nv;
-      if (kt == 0 || kt == 32) reinterpret_cast<uint16_t *>(&s_nv[sb][1])[kt >> 5] = nan;
+      if (t + kPfxLoaders < jobs) fetch(t + kPfxLoaders);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&k_full[slot]);
-        mbar_arrive(&sc_full[sb]);
-      }
-      return true;
-    };
-    fetch(0, buf[0]);
-    if (n > 1) fetch(1, buf[1]);
-    for (int j = 0; j < n && ok; j += 2) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (j + u >= n) break;
-        if (!put(j + u, buf[u])) { ok = false; break; }
-        if (j + u + 2 < n) fetch(j + u + 2, buf[u]);
+        mbar_arrive(&full[slot]);
+        if (k) mbar_arrive(&sc_full[sb]);
       }
     }
     if constexpr (!PV) {
@@ -426,91 +490,61 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       svm = __reduce_max_sync(0xffffffffu, svm);
       if (lane == 0 && svm != 0) atomicMax(&p.svmax[h], svm << 16);
     }
-  } else if (warp < 12) {
-    // ------------------------------------ V ------------------------------------
-    if constexpr (PV) {
-      const int vt = tid - 256;
-      constexpr int NL = D / 32;                     // load x is row vt / 4 + 32 x
-      const int rw0 = vt >> 2, c0 = (vt & 3) * 2;
-      const uint32_t d0 = rw0 * 128 + ((c0 ^ (rw0 & 7)) << 4), d1 = rw0 * 128 + (((c0 + 1) ^ (rw0 & 7)) << 4);
-      uint4 buf[2][NL];
-      auto fetch = [&](int j, uint4 *r) {
-        int page = p.ptable[j0 + j];
-        if (page < 0 || page >= p.q8.n_pages) page = 0;   // its keys weigh nothing
-        const int8_t *src = p.q8.v + ((size_t)page * H + h) * 64 * D + vt * 16;
-#pragma unroll
-        for (int x = 0; x < NL; ++x) r[x] = q8_ldg(src + x * 2048);
-      };
-      auto put = [&](int j, const uint4 *r) {
-        const int slot = j & 1;
-        if (j >= 2 && !mbar_wait(&v_empty[slot], ((j >> 1) - 1) & 1)) return false;
-        uint8_t *dst = pfx_sm + L::v + slot * L::kV;
-#pragma unroll
-        for (int x = 0; x < NL; ++x) {
-          uint4 lo, hi;
-          pfx_f16(r[x], lo, hi);
-          *reinterpret_cast<uint4 *>(dst + d0 + x * 32 * 128) = lo;
-          *reinterpret_cast<uint4 *>(dst + d1 + x * 32 * 128) = hi;
+  } else {
+    reg_dec<24>();
+    if (warp == 20 && lane == 0) {
+      // ------------------------------- MMA issuer -------------------------------
+      constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_o = umma_idesc_f16(128, D);
+      const uint32_t ring = smem_u32(pfx_sm);
+      int t = 0;                                     // the ring's jobs, in the loaders' order
+      auto qk = [&](int j) {
+        const int slot = t % R, ss = j % NS;
+        if (!mbar_wait(&full[slot], (t / R) & 1)) return false;
+        if (!PV && j >= NS && !mbar_wait(&s_empty[ss], ((j / NS) - 1) & 1)) return false;
+        // S j - 2 holds the weights of w V j - 2: that product has to be done
+        if (PV && j >= 2) {
+          const int tv = 2 * (j - 1);                // its V's job
+          if (!mbar_wait(&empty[tv % R], (tv / R) & 1)) return false;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[slot]);
+        tc_fence_after();
+        const uint32_t acc = tmem + L::ts + 64 * ss, kb = ring + slot * L::kSlot;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_f16_ta(acc, tmem + L::tq + 32 * i + 8 * k, umma_desc_sw128(kb + i * 64 * 128 + 32 * k),
+                          id_s, i > 0 || k > 0);
+        tc_commit(&empty[slot]);
+        tc_commit(&s_full[ss]);
+        ++t;
         return true;
       };
-      fetch(0, buf[0]);
-      if (n > 1) fetch(1, buf[1]);
-      for (int j = 0; j < n && ok; j += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (j + u >= n) break;
-          if (!put(j + u, buf[u])) { ok = false; break; }
-          if (j + u + 2 < n) fetch(j + u + 2, buf[u]);
-        }
-      }
-    }
-  } else if (lane == 0) {
-    // ------------------------------- MMA issuer -------------------------------
-    constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_o = umma_idesc_f16(128, D);
-    const uint32_t q0 = smem_u32(pfx_sm + L::q), k0 = smem_u32(pfx_sm + L::k);
-    const uint32_t v0 = smem_u32(pfx_sm + L::v), w0 = smem_u32(pfx_sm + L::w);
-    auto weights_v = [&](int j) {
-      const int slot = j & 1;
-      if (!mbar_wait(&w_full[slot], (j >> 1) & 1) || !mbar_wait(&v_full[slot], (j >> 1) & 1)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma_f16(tmem, umma_desc_sw128(w0 + slot * L::kTile + 32 * k),
-                   umma_desc_sw128(v0 + slot * L::kV + 32 * k), id_o, j > 0 || k > 0);
-      tc_commit(&v_empty[slot]);                     // frees the slot's V and weights
-      return true;
-    };
-    for (int j = 0; j < n && ok; ++j) {
-      const int slot = j % NK, sb = j & 3;
-      if (!mbar_wait(&k_full[slot], (j / NK) & 1)) { ok = false; break; }
-      if (j >= 4 && !mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1)) { ok = false; break; }
-      tc_fence_after();
-      const uint32_t acc = tmem + (PV ? 256 : 0) + 64 * sb, kb = k0 + slot * L::kPage;
-#pragma unroll
-      for (int i = 0; i < DB; ++i)
+      auto wv = [&](int j) {
+        const int slot = t % R, ss = j % NS;
+        if (!mbar_wait(&w_full[ss], (j / NS) & 1) || !mbar_wait(&full[slot], (t / R) & 1)) return false;
+        tc_fence_after();
+        const uint32_t vb = ring + slot * L::kSlot;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma_f16(acc, umma_desc_sw128(q0 + i * L::kTile + 32 * k),
-                     umma_desc_sw128(kb + i * 64 * 128 + 32 * k), id_s, i > 0 || k > 0);
-      tc_commit(&k_empty[slot]);
-      tc_commit(&s_full[sb]);
-      if constexpr (PV)
-        if (j >= kPfxAhead && !weights_v(j - kPfxAhead)) { ok = false; break; }
+          tc_mma_f16_ta(tmem, tmem + L::ts + 64 * ss + 8 * k, umma_desc_sw128(vb + 32 * k), id_o, j > 0 || k > 0);
+        tc_commit(&empty[slot]);
+        ++t;
+        return true;
+      };
+      ok = qk(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) ok = qk(j + 1);
+        if constexpr (PV) ok = ok && wv(j);
+      }
+      if constexpr (PV) tc_commit(o_full);
     }
-    if constexpr (PV) {
-      for (int j = max(0, n - kPfxAhead); j < n && ok; ++j) ok = weights_v(j);
-      tc_commit(o_full);
-    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     tc_fence_after();
-    tmem_dealloc(tmem, PV ? 512 : 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
