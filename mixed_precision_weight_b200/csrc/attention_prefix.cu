@@ -89,14 +89,30 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16 (A: two FP16 per 32-bit column)
-__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16 (A: two FP16 per 32-bit column).
+// The whole warp runs the issuing code and one lane (`lead`) is predicated in: the
+// operands then live in uniform registers (a branch on the lane cost 100 cycles
+// per product issued).
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
+                                              uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ void tc_commit_lead(uint32_t lead, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r;
 }
 
 template <int N>
@@ -130,6 +146,68 @@ __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// A row's 64 products of one page: their largest logit over ks (a NaN is passed over).
+// Whole: all 64 keys are live.
+template <bool Whole>
+__device__ __forceinline__ float pfx_page_max(const uint32_t *s, const float *ks, int nv) {
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 64; i += 4) {
+    const float4 a = *reinterpret_cast<const float4 *>(ks + i);
+    const float2 x = mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y));
+    const float2 y = mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w));
+    if (Whole || i < nv) m0 = fmaxf(m0, x.x);
+    if (Whole || i + 1 < nv) m0 = fmaxf(m0, x.y);
+    if (Whole || i + 2 < nv) m1 = fmaxf(m1, y.x);
+    if (Whole || i + 3 < nv) m1 = fmaxf(m1, y.y);
+  }
+  return fmaxf(m0, m1);
+}
+
+// A row's weights of one page, FP16 pairs exp2(S ks r2 + x0) vs, and the sum of the
+// exponentials.  Whole: all 64 keys are live and no value scale is a NaN.  The two
+// bodies are apart so that each is one straight block for the scheduler: with the
+// choice inside the loop a page took 2700 cycles.
+template <bool Whole>
+__device__ __forceinline__ float2 pfx_page_weights(const uint32_t *s, const float *ks, const float *vs,
+                                                   int nv, float r2, float x0, float floor2, uint32_t *w) {
+  const float2 rr = make_float2(r2, r2), xx = make_float2(x0, x0);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 64; i += 4) {
+    const float4 a = *reinterpret_cast<const float4 *>(ks + i);
+    const float4 v = *reinterpret_cast<const float4 *>(vs + i);
+    const float2 x = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y)), rr, xx);
+    const float2 y = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w)), rr, xx);
+    float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    float2 ey = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    float2 wx, wy;
+    // below the haze threshold: dropped (a NaN logit is kept)
+    if (x.x < floor2) ex.x = 0.f;
+    if (x.y < floor2) ex.y = 0.f;
+    if (y.x < floor2) ey.x = 0.f;
+    if (y.y < floor2) ey.y = 0.f;
+    if (Whole) {
+      wx = mat_mul2(ex, make_float2(v.x, v.y));
+      wy = mat_mul2(ey, make_float2(v.z, v.w));
+    } else {
+      // keys past the prefix's end weigh nothing, and the value scale of a key
+      // without weight is not looked at
+      if (i >= nv) ex.x = 0.f;
+      if (i + 1 >= nv) ex.y = 0.f;
+      if (i + 2 >= nv) ey.x = 0.f;
+      if (i + 3 >= nv) ey.y = 0.f;
+      wx = make_float2(ex.x == 0.f ? 0.f : ex.x * v.x, ex.y == 0.f ? 0.f : ex.y * v.y);
+      wy = make_float2(ey.x == 0.f ? 0.f : ey.x * v.z, ey.y == 0.f ? 0.f : ey.y * v.w);
+    }
+    sum = mat_add2(sum, mat_add2(ex, ey));
+    const __half2 ox = __floats2half2_rn(wx.x, wx.y), oy = __floats2half2_rn(wy.x, wy.y);
+    w[i / 2] = *reinterpret_cast<const uint32_t *>(&ox);
+    w[i / 2 + 1] = *reinterpret_cast<const uint32_t *>(&oy);
+  }
+  return sum;
 }
 
 template <int D, bool PV>
@@ -297,57 +375,12 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       tmem_ld_wait32(s);
       tmem_ld_wait32(s + 32);
       if constexpr (!PV) {
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(&s_a[sb][i]);
-          const float2 x = mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y));
-          const float2 y = mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w));
-          if (nv == 64) {
-            mx = fmaxf(fmaxf(mx, fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
-          } else {
-            if (i < nv) mx = fmaxf(mx, x.x);
-            if (i + 1 < nv) mx = fmaxf(mx, x.y);
-            if (i + 2 < nv) mx = fmaxf(mx, y.x);
-            if (i + 3 < nv) mx = fmaxf(mx, y.y);
-          }
-        }
+        if (nv == 64) mx = fmaxf(mx, pfx_page_max<true>(s, s_a[sb], nv));
+        else mx = fmaxf(mx, pfx_page_max<false>(s, s_a[sb], nv));
       } else {
-        const float2 rr2 = make_float2(r2, r2), xx0 = make_float2(x0, x0);
         uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(&s_a[sb][i]);
-          const float4 v = *reinterpret_cast<const float4 *>(&s_v[sb][i]);
-          const float2 x = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
-                                             make_float2(a.x, a.y)), rr2, xx0);
-          const float2 y = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])),
-                                             make_float2(a.z, a.w)), rr2, xx0);
-          float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-          float2 ey = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-          float2 wx, wy;
-          // below the haze threshold: dropped (a NaN logit is kept)
-          if (x.x < floor2) ex.x = 0.f;
-          if (x.y < floor2) ex.y = 0.f;
-          if (y.x < floor2) ey.x = 0.f;
-          if (y.y < floor2) ey.y = 0.f;
-          if (plain) {
-            wx = mat_mul2(ex, make_float2(v.x, v.y));
-            wy = mat_mul2(ey, make_float2(v.z, v.w));
-          } else {
-            // keys past the prefix's end weigh nothing, and the value scale of a key
-            // without weight is not looked at
-            if (i >= nv) ex.x = 0.f;
-            if (i + 1 >= nv) ex.y = 0.f;
-            if (i + 2 >= nv) ey.x = 0.f;
-            if (i + 3 >= nv) ey.y = 0.f;
-            wx = make_float2(ex.x == 0.f ? 0.f : ex.x * v.x, ex.y == 0.f ? 0.f : ex.y * v.y);
-            wy = make_float2(ey.x == 0.f ? 0.f : ey.x * v.z, ey.y == 0.f ? 0.f : ey.y * v.w);
-          }
-          sum = mat_add2(sum, mat_add2(ex, ey));
-          const __half2 ox = __floats2half2_rn(wx.x, wx.y), oy = __floats2half2_rn(wy.x, wy.y);
-          w[i / 2] = *reinterpret_cast<const uint32_t *>(&ox);
-          w[i / 2 + 1] = *reinterpret_cast<const uint32_t *>(&oy);
-        }
+        if (plain) sum = mat_add2(sum, pfx_page_weights<true>(s, s_a[sb], s_v[sb], nv, r2, x0, floor2, w));
+        else sum = mat_add2(sum, pfx_page_weights<false>(s, s_a[sb], s_v[sb], nv, r2, x0, floor2, w));
         tmem_st32(src, w);                           // over this row's S
         tmem_st_wait();
       }
@@ -492,43 +525,51 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     }
   } else {
     reg_dec<24>();
-    if (warp == 20 && lane == 0) {
+    if (warp == 20) {
       // ------------------------------- MMA issuer -------------------------------
       constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_o = umma_idesc_f16(128, D);
-      const uint32_t ring = smem_u32(pfx_sm);
-      int t = 0;                                     // the ring's jobs, in the loaders' order
+      const uint32_t lead = elect_one();
+      const uint64_t desc = umma_desc_sw128(smem_u32(pfx_sm));   // addresses below 256 KB: sums do not carry
+      int t = 0, slot = 0, par = 0;                  // the ring's jobs, in the loaders' order
+      auto next = [&] {
+        ++t;
+        if (++slot == R) { slot = 0; par ^= 1; }
+      };
       auto qk = [&](int j) {
-        const int slot = t % R, ss = j % NS;
-        if (!mbar_wait(&full[slot], (t / R) & 1)) return false;
-        if (!PV && j >= NS && !mbar_wait(&s_empty[ss], ((j / NS) - 1) & 1)) return false;
+        const int ss = j % NS;
+        bool got = mbar_wait(&full[slot], par);
+        if (!PV && j >= NS) got = got && mbar_wait(&s_empty[ss], ((j / NS) - 1) & 1);
         // S j - 2 holds the weights of w V j - 2: that product has to be done
         if (PV && j >= 2) {
           const int tv = 2 * (j - 1);                // its V's job
-          if (!mbar_wait(&empty[tv % R], (tv / R) & 1)) return false;
+          got = got && mbar_wait(&empty[tv % R], (tv / R) & 1);
         }
+        if (!__all_sync(0xffffffffu, got)) return false;
         tc_fence_after();
-        const uint32_t acc = tmem + L::ts + 64 * ss, kb = ring + slot * L::kSlot;
+        const uint32_t acc = tmem + L::ts + 64 * ss;
+        const uint64_t kb = desc + (uint64_t)(slot * (L::kSlot >> 4));
 #pragma unroll
         for (int i = 0; i < DB; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_f16_ta(acc, tmem + L::tq + 32 * i + 8 * k, umma_desc_sw128(kb + i * 64 * 128 + 32 * k),
+            tc_mma_f16_ta(lead, acc, tmem + L::tq + 32 * i + 8 * k, kb + (uint64_t)(i * 512 + 2 * k),
                           id_s, i > 0 || k > 0);
-        tc_commit(&empty[slot]);
-        tc_commit(&s_full[ss]);
-        ++t;
+        tc_commit_lead(lead, &empty[slot]);
+        tc_commit_lead(lead, &s_full[ss]);
+        next();
         return true;
       };
       auto wv = [&](int j) {
-        const int slot = t % R, ss = j % NS;
-        if (!mbar_wait(&w_full[ss], (j / NS) & 1) || !mbar_wait(&full[slot], (t / R) & 1)) return false;
+        const int ss = j % NS;
+        const bool got = mbar_wait(&w_full[ss], (j / NS) & 1) && mbar_wait(&full[slot], par);
+        if (!__all_sync(0xffffffffu, got)) return false;
         tc_fence_after();
-        const uint32_t vb = ring + slot * L::kSlot;
+        const uint64_t vb = desc + (uint64_t)(slot * (L::kSlot >> 4));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma_f16_ta(tmem, tmem + L::ts + 64 * ss + 8 * k, umma_desc_sw128(vb + 32 * k), id_o, j > 0 || k > 0);
-        tc_commit(&empty[slot]);
-        ++t;
+          tc_mma_f16_ta(lead, tmem, tmem + L::ts + 64 * ss + 8 * k, vb + (uint64_t)(2 * k), id_o, j > 0 || k > 0);
+        tc_commit_lead(lead, &empty[slot]);
+        next();
         return true;
       };
       ok = qk(0);
@@ -536,9 +577,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         if (j + 1 < n) ok = qk(j + 1);
         if constexpr (PV) ok = ok && wv(j);
       }
-      if constexpr (PV) tc_commit(o_full);
+      if constexpr (PV) tc_commit_lead(lead, o_full);
     }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
