@@ -11,14 +11,14 @@
 // and q8_merge adds the items' and the splits' partials in order.
 //
 // A CTA holds 128 rows of Q and walks a split of the prefix page by page (64
-// keys).  Warps 0-7 turn S into weights (a warpgroup per page, alternating, a
-// thread per row); warps 8-19 bring pages from global memory through registers,
-// where the 8-bit codes become FP16, into a ring of 128-byte-swizzled shared
-// memory (a warpgroup per page, in the order the products take them); one thread
-// of warp 20 issues the MMAs.  Q lies in tensor memory and the weights overwrite
-// their S there, so that both products read one operand only from shared memory:
-// with Q there too, a 128 x 64 x 16 product took 66 cycles instead of 32, its
-// operands' bytes at 128 per cycle.  Q K^T of page j + 1 is issued before w V of
+// keys).  Converting warpgroups bring pages from global memory through registers,
+// where the 8-bit codes become FP16, into a ring of 128-byte-swizzled tiles (a
+// warpgroup per page in turn, in the order the products take them); one warp
+// issues the MMAs; warps 0-7 turn S into weights (a thread per row, a warpgroup per
+// half of the page's keys).  Q lies in tensor memory and the weights overwrite
+// their S there, so that both products read one operand only from shared memory,
+// whose bandwidth bounds a page (64 KB of tiles written, 64 KB read; staging the
+// raw codes there too was slower).  Q K^T of page j + 1 is issued before w V of
 // page j.
 //
 // Number formats: a code is exact in FP16 (1024 + u from a byte permutation,
@@ -32,9 +32,9 @@
 
 namespace dvssq {
 
-constexpr int kPfxThreads = 6 * 128;     // two weight, three loading and one issuing warpgroup
-constexpr int kPfxLoaders = 3;
-constexpr int kPfxRing = 6;              // pages of FP16 codes in shared memory
+constexpr int kPfxConv = 3;              // converting warpgroups
+constexpr int kPfxThreads = (3 + kPfxConv) * 128;   // two of weights and one that issues beside them
+constexpr int kPfxMma = 4 * (2 + kPfxConv);         // the issuing warp
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct PfxParams {
@@ -85,6 +85,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t r[32]) 
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t r[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :
+               : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                 "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -115,15 +122,6 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // 16 codes -> 16 FP16 values in order, as two 16-byte chunks
 __device__ __forceinline__ void pfx_f16(const uint4 &c, uint4 &lo, uint4 &hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -148,13 +146,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// A row's 64 products of one page: their largest logit over ks (a NaN is passed over).
-// Whole: all 64 keys are live.
+// A row's 32 products of half a page: their largest logit over ks (a NaN is passed over).
+// Whole: all the page's keys are live; else the half's first nv are.
 template <bool Whole>
-__device__ __forceinline__ float pfx_page_max(const uint32_t *s, const float *ks, int nv) {
+__device__ __forceinline__ float pfx_half_max(const uint32_t *s, const float *ks, int nv) {
   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 64; i += 4) {
+  for (int i = 0; i < 32; i += 4) {
     const float4 a = *reinterpret_cast<const float4 *>(ks + i);
     const float2 x = mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y));
     const float2 y = mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w));
@@ -166,17 +164,17 @@ __device__ __forceinline__ float pfx_page_max(const uint32_t *s, const float *ks
   return fmaxf(m0, m1);
 }
 
-// A row's weights of one page, FP16 pairs exp2(S ks r2 + x0) vs, and the sum of the
-// exponentials.  Whole: all 64 keys are live and no value scale is a NaN.  The two
+// A row's weights of a quarter of a page (16 keys), FP16 pairs exp2(S ks r2 + x0) vs,
+// and the sum of the exponentials.  Whole: all the page's keys are live and no value scale is a NaN.  The two
 // bodies are apart so that each is one straight block for the scheduler: with the
-// choice inside the loop a page took 2700 cycles.
+// choice inside the loop 64 keys took 2700 cycles instead of 1700.
 template <bool Whole>
-__device__ __forceinline__ float2 pfx_page_weights(const uint32_t *s, const float *ks, const float *vs,
+__device__ __forceinline__ float2 pfx_weights16(const uint32_t *s, const float *ks, const float *vs,
                                                    int nv, float r2, float x0, float floor2, uint32_t *w) {
   const float2 rr = make_float2(r2, r2), xx = make_float2(x0, x0);
   float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 64; i += 4) {
+  for (int i = 0; i < 16; i += 4) {
     const float4 a = *reinterpret_cast<const float4 *>(ks + i);
     const float4 v = *reinterpret_cast<const float4 *>(vs + i);
     const float2 x = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y)), rr, xx);
@@ -213,15 +211,17 @@ __device__ __forceinline__ float2 pfx_page_weights(const uint32_t *s, const floa
 template <int D, bool PV>
 struct PfxSmem {
   static constexpr int DB = D / 64;
-  static constexpr int kSlot = D * 128;                  // a page: K [DB][64 rows][128 B] or V [D rows][128 B]
-  static constexpr int kQRow = 2 * D + 16;               // a staged row of Q (in the ring, before it fills)
-  static constexpr int sa = kPfxRing * kSlot;            // float [4][64]: key scales
+  static constexpr int R = 6;                            // FP16 pages
+  static constexpr int kSlot = D * 128;                  // FP16: K [DB][64 rows][128 B] or V [D rows][128 B]
+  static constexpr int kQRow = 2 * D + 16;               // a staged row of Q (in the FP16 ring, before it fills)
+  static constexpr int sa = R * kSlot;                   // float [4][64]: key scales
   static constexpr int sv = sa + 4 * 64 * 4;             // float [4][64]: value scales
   static constexpr int step = sv + 4 * 64 * 4;           // float [128]
   static constexpr int nv = step + 128 * 4;              // int [4][2]: live keys, NaN value scales
   static constexpr int bar = nv + 32;
-  static constexpr int bytes = bar + (2 * kPfxRing + 15) * 8 + 16;
-  static_assert(128 * kQRow <= kPfxRing * kSlot && 8 * 32 * 36 * 4 <= kPfxRing * kSlot, "staging fits the ring");
+  static constexpr int bytes = bar + (2 * R + 15) * 8 + 16;
+  static_assert(128 * kQRow <= R * kSlot && 8 * 32 * 36 * 4 <= R * kSlot, "staging fits the ring");
+  static_assert(bytes <= 232448, "shared memory of one CTA");
   // tensor memory columns: O, then Q, then the S buffers (64 columns each)
   static constexpr int NS = PV ? 2 : 4;
   static constexpr int tq = PV ? 256 : 0;
@@ -231,7 +231,7 @@ struct PfxSmem {
 template <int D, bool PV>
 __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) {
   using L = PfxSmem<D, PV>;
-  constexpr int DB = L::DB, VPL = D / 32, NS = L::NS, R = kPfxRing;
+  constexpr int DB = L::DB, VPL = D / 32, NS = L::NS, R = L::R;
   extern __shared__ __align__(1024) uint8_t pfx_sm[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(pfx_sm + L::bar);
   uint64_t *full = bar, *empty = bar + R, *s_full = bar + 2 * R, *s_empty = s_full + 4,
@@ -250,6 +250,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     if (tid == 0) set_error(kErrBadShape);
     return;
   }
+  // jobs in the order of the products: K(0), then K(j + 1), V(j), .., V(n - 1)
+  const int jobs = PV ? 2 * n : n;
+  auto is_k = [&](int t) { return !PV || t == 0 || ((t & 1) && t < 2 * n - 1); };
+  auto page_of = [&](int t) { return !PV ? t : t == 2 * n - 1 ? n - 1 : is_k(t) ? (t + 1) >> 1 : (t >> 1) - 1; };
   if (tid == 0) {
     for (int s = 0; s < R; ++s) {
       mbar_init(&full[s], 4);
@@ -257,26 +261,26 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&s_empty[s], 4);
+      mbar_init(&s_empty[s], 8);
       mbar_init(&sc_full[s], 4);
     }
-    mbar_init(&w_full[0], 4);
-    mbar_init(&w_full[1], 4);
+    mbar_init(&w_full[0], 8);
+    mbar_init(&w_full[1], 8);
     mbar_init(o_full, 1);
     fence_mbarrier_init();
   }
-  if (warp == 20) {
+  if (warp == kPfxMma) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   // Q: a warp per row, all its rows in flight; row r of the tile is query head
   // h G + r % G of sequence r / G.  Staged as FP16 rows, then into tensor memory.
   {
-    constexpr int NR = 6;                    // 24 warps, 128 rows
+    constexpr int NWARP = kPfxThreads / 32, NR = (128 + NWARP - 1) / NWARP;
     KvRaw<VPL> raw[NR];
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
-      const int r = warp + 24 * u, rr = rt * 128 + r;
+      const int r = warp + NWARP * u, rr = rt * 128 + r;
 #pragma unroll
       for (int i = 0; i < VPL / 2; ++i) raw[u].w[i] = 0;
       if (r < 128 && rr < p.rows) {
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     }
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
-      const int r = warp + 24 * u;
+      const int r = warp + NWARP * u;
       if (r >= 128) break;
       uint32_t m = 0;
 #pragma unroll
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
   if (warp < 4) {
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < DB; ++j) {
       uint32_t w[32];
 #pragma unroll
@@ -332,7 +336,6 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
 
   if (wg < 2) {
     // ------------------------------- weights -------------------------------
-    reg_inc<112>();
     const int row = tid & 127, rr = rt * 128 + row;
     const bool live = rr < p.rows;
     const int b = live ? rr / G : 0, hq = h * G + (live ? rr - b * G : 0);
@@ -360,28 +363,32 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     }
     const float r2 = r1 * kLog2e;
-    for (int j = wg; j < n && ok; j += 2) {
+    for (int j = 0; j < n && ok; ++j) {
       const int sb = j & 3, ss = j % NS;
       const bool got = mbar_wait(&sc_full[sb], (j >> 2) & 1) && mbar_wait(&s_full[ss], (j / NS) & 1);
       // a warp gives up as one: the tensor-memory loads are warp-wide
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
-      const int nv = s_nv[sb][0];
-      const bool plain = nv == 64 && (s_nv[sb][1] == 0);
-      const uint32_t src = lane_base + L::ts + 64 * ss;
-      uint32_t s[64];
+      const int nv = s_nv[sb][0], live_keys = nv - 32 * wg;
+      const uint32_t src = lane_base + L::ts + 64 * ss + 32 * wg;
+      const float *ks = s_a[sb] + 32 * wg, *vs = s_v[sb] + 32 * wg;
+      uint32_t s[32];
       tmem_ld32(src, s);
-      tmem_ld32(src + 32, s + 32);
       tmem_ld_wait32(s);
-      tmem_ld_wait32(s + 32);
       if constexpr (!PV) {
-        if (nv == 64) mx = fmaxf(mx, pfx_page_max<true>(s, s_a[sb], nv));
-        else mx = fmaxf(mx, pfx_page_max<false>(s, s_a[sb], nv));
+        if (nv == 64) mx = fmaxf(mx, pfx_half_max<true>(s, ks, live_keys));
+        else mx = fmaxf(mx, pfx_half_max<false>(s, ks, live_keys));
       } else {
-        uint32_t w[32];
-        if (plain) sum = mat_add2(sum, pfx_page_weights<true>(s, s_a[sb], s_v[sb], nv, r2, x0, floor2, w));
-        else sum = mat_add2(sum, pfx_page_weights<false>(s, s_a[sb], s_v[sb], nv, r2, x0, floor2, w));
-        tmem_st32(src, w);                           // over this row's S
+        const bool whole = nv == 64 && s_nv[sb][1] == 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[8];
+          if (whole)
+            sum = mat_add2(sum, pfx_weights16<true>(s + 16 * c, ks + 16 * c, vs + 16 * c, 16, r2, x0, floor2, w));
+          else
+            sum = mat_add2(sum, pfx_weights16<false>(s + 16 * c, ks + 16 * c, vs + 16 * c, live_keys - 16 * c, r2, x0, floor2, w));
+          tmem_st8(src + 8 * c, w);                  // over this thread's S
+        }
         tmem_st_wait();
       }
       tc_fence_before();
@@ -432,35 +439,33 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     }
     tc_fence_before();
-  } else if (wg < 2 + kPfxLoaders) {
-    // ------------------------- pages into the ring -------------------------
-    reg_dec<72>();
-    const int kt = tid & 127, jobs = PV ? 2 * n : n;
-    constexpr int NL = D / 32;                       // 16-byte loads per thread and page
+  } else if (wg < 2 + kPfxConv) {
+    // --------------------------- codes to FP16 tiles ---------------------------
+    const int kt = tid & 127;
+    constexpr int NL = D / 32;                       // 16-byte pieces per thread and page
     constexpr int CPR = D / 16;                      // 16-byte pieces of a K row
-    // K piece: load x is row kr + x (128 / CPR), piece ch; FP16 pieces 2 c and 2 c + 1 of
-    // the row; lanes 4-7 store the odd one first, so that eight lanes meet the
-    // eight 16-byte columns
+    // K: piece x is in row kr + x (128 / CPR), place ch; FP16 pieces 2 c and 2 c + 1 of the
+    // row; lanes 4-7 store the odd one first, so that eight lanes meet the eight
+    // 16-byte columns
     const int ch = kt % CPR, kr = kt / CPR, odd = (ch >> 2) & 1;
     const uint32_t kat = (ch >> 2) * 64 * 128 + kr * 128;
     const uint32_t k0 = kat + ((((ch & 3) * 2 + odd) ^ (kr & 7)) << 4);
     const uint32_t k1 = kat + ((((ch & 3) * 2 + 1 - odd) ^ (kr & 7)) << 4);
-    // V piece: load x is row kt / 4 + 32 x
+    // V: piece x is in row kt / 4 + 32 x
     const int vr = kt >> 2;
     const uint32_t v0 = vr * 128 + ((((kt & 3) * 2) ^ (vr & 7)) << 4);
     const uint32_t v1 = vr * 128 + ((((kt & 3) * 2 + 1) ^ (vr & 7)) << 4);
-    // jobs in the order of the products: K(0), then K(j + 1), V(j), .., V(n - 1)
-    auto is_k = [&](int t) { return !PV || t == 0 || ((t & 1) && t < 2 * n - 1); };
-    auto page_of = [&](int t) { return !PV ? t : t == 2 * n - 1 ? n - 1 : is_k(t) ? (t + 1) >> 1 : (t >> 1) - 1; };
-    uint4 r[NL];
-    uint16_t ks = 0, vs = 0;
-    int nv = 0;
     uint32_t svm = 0;
+    // a job's codes (and a K page's scales) into registers; page ids one job ahead
+    uint4 r[NL];
+    uint32_t ks = 0, vs = 0;
+    int nv = 0, ahead = 0;
+    auto page_id = [&](int t) { return t < jobs ? p.ptable[j0 + page_of(t)] : 0; };
     auto fetch = [&](int t) {
-      const int w = j0 + page_of(t);
       const bool k = is_k(t);
-      int page = p.ptable[w];
-      nv = min(64, p.prefix - 64 * w);
+      int page = ahead;
+      ahead = page_id(t + kPfxConv);
+      nv = min(64, p.prefix - 64 * (j0 + page_of(t)));
       if (page < 0 || page >= p.q8.n_pages) {        // its keys weigh nothing
         set_error(kErrBadIndex);
         page = nv = 0;
@@ -475,12 +480,17 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     };
     int t = wg - 2;
+    ahead = page_id(t);
     if (t < jobs) fetch(t);
-    for (; t < jobs && ok; t += kPfxLoaders) {
+    for (; t < jobs && ok; t += kPfxConv) {
       const int slot = t % R, j = page_of(t), sb = j & 3;
-      if (t >= R && !mbar_wait(&empty[slot], ((t / R) - 1) & 1)) { ok = false; break; }
-      uint8_t *dst = pfx_sm + slot * L::kSlot;
       const bool k = is_k(t);
+      bool got = true;
+      if (t >= R) got = mbar_wait(&empty[slot], ((t / R) - 1) & 1);
+      // the weights of page j - 4 are done with this slot of scales
+      if (k && j >= 4) got = got && mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1);
+      if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+      uint8_t *dst = pfx_sm + slot * L::kSlot;
       if (k) {
 #pragma unroll
         for (int x = 0; x < NL; ++x) {
@@ -490,9 +500,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
           *reinterpret_cast<uint4 *>(dst + k0 + o) = odd ? hi : lo;
           *reinterpret_cast<uint4 *>(dst + k1 + o) = odd ? lo : hi;
         }
-        // the weights of page j - 4 are done with this slot of scales
-        if (j >= 4 && !mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1)) { ok = false; break; }
-        if ((kt & 63) < nv && vs < 0x7F80u) svm = max(svm, (uint32_t)vs);
+        if ((kt & 63) < nv && vs < 0x7F80u) svm = max(svm, vs);
         const bool nan = __any_sync(0xffffffffu, vs >= 0x7F80u);
         if (kt < 64) {
           s_a[sb][kt] = bf16_bits_to_f32(ks);
@@ -509,7 +517,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
           *reinterpret_cast<uint4 *>(dst + v1 + x * 32 * 128) = hi;
         }
       }
-      if (t + kPfxLoaders < jobs) fetch(t + kPfxLoaders);
+      if (t + kPfxConv < jobs) fetch(t + kPfxConv);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -524,8 +532,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       if (lane == 0 && svm != 0) atomicMax(&p.svmax[h], svm << 16);
     }
   } else {
-    reg_dec<24>();
-    if (warp == 20) {
+    if (warp == kPfxMma) {
       // ------------------------------- MMA issuer -------------------------------
       constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_o = umma_idesc_f16(128, D);
       const uint32_t lead = elect_one();
@@ -566,8 +573,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         tc_fence_after();
         const uint64_t vb = desc + (uint64_t)(slot * (L::kSlot >> 4));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma_f16_ta(lead, tmem, tmem + L::ts + 64 * ss + 8 * k, vb + (uint64_t)(2 * k), id_o, j > 0 || k > 0);
+        for (int k = 0; k < 4; ++k)                  // keys 0-31 lie over S columns 0 .., keys 32-63 over 32 ..
+          tc_mma_f16_ta(lead, tmem, tmem + L::ts + 64 * ss + 8 * k + (k < 2 ? 0 : 16), vb + (uint64_t)(2 * k), id_o,
+                        j > 0 || k > 0);
         tc_commit_lead(lead, &empty[slot]);
         next();
         return true;
@@ -582,7 +590,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 20) {
+  if (warp == kPfxMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
