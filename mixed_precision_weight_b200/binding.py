@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 import torch
@@ -377,54 +378,68 @@ def dvssq_bss_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tau: 
 
 KV_PAGE = 64
 
-
-def _launch(device, stream, body):
-    """body(stream handle) with ``device`` current; new tensors belong to ``stream``."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
-    with torch.cuda.device(device):
-        if stream is None:
-            return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
-        s = stream
-        if not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(int(stream), device=device)
-        if s.device != device:
-            raise ValueError(f"the stream belongs to {s.device}, the tensors to {device}")
-        with torch.cuda.stream(s):
-            return body(ctypes.c_void_p(s.cuda_stream))
+# The calls below sit in decode loops of a few microseconds: they read the current
+# device and stream without building torch objects, and keep the checks to plain
+# attribute reads.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _indices(t, name, n, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+class _on:
+    """With-block: ``index`` is the current device and ``stream`` (None: that device's
+    current one) the current stream, so that new tensors belong to it."""
+
+    def __init__(self, index, stream):
+        self._device = torch.cuda.device(index)
+        self._stream = None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=f"cuda:{index}")
+            if stream.device.index != index:
+                raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{index}")
+            self._stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+
+    def __exit__(self, *e):
+        if self._stream is not None:
+            self._stream.__exit__(*e)
+        self._device.__exit__(*e)
+
+
+def _indices(t, name, n, index):
+    """Pointer of n contiguous int32 values on CUDA device ``index`` (-1: the host)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         raise TypeError(f"{name} must be an int32 tensor")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and hold {n} values, got shape {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    return ctypes.c_void_p(t.data_ptr())
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
+    return t.data_ptr()
 
 
-def _rows(t, name, shape, device):
+def _rows(t, name, shape, index):
     """Pointer and (outer, head) strides of BF16 rows [n][heads][d] whose last axis is contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
     a, b, c = t.stride()
     if c != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
     # the stride of an axis of length one is never used
-    return ctypes.c_void_p(t.data_ptr()), 0 if shape[0] == 1 else a, 0 if shape[1] == 1 else b
+    return t.data_ptr(), 0 if shape[0] == 1 else a, 0 if shape[1] == 1 else b
 
 
-def _result(t, name, shape, dtype, device):
-    """``t``, checked, or a new tensor: a call's contiguous result."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+def _given(t, name, shape, dtype, index):
+    """Checks a caller's result tensor."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on cuda:{index}")
     return t
 
 
@@ -435,31 +450,42 @@ class KvCache:
     ``k`` int8 [pages][kv_heads][64][d], ``v`` int8 [pages][kv_heads][d][64],
     ``k_scale`` and ``v_scale`` bfloat16 [pages][kv_heads][64], ``table`` int32
     [batch][width], all contiguous and on one CUDA device.  The caller owns the
-    assignment of pages; several KvCache objects may share a pool.
+    assignment of pages; several KvCache objects may share a pool.  The tensors
+    are read at construction: a cache on other tensors is another KvCache.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "table", "device", "_c")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_table", "index", "batch", "width", "kv_heads",
+                 "head_dim", "_c", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale, table):
         if k.dim() != 4 or table.dim() != 2:
             raise ValueError("k must be [pages][kv_heads][64][d] and table [batch][width]")
-        P, H, page, d = k.shape
-        dev = k.device
-        want = ((k, "k", torch.int8, (P, H, KV_PAGE, d)), (v, "v", torch.int8, (P, H, d, KV_PAGE)),
-                (k_scale, "k_scale", torch.bfloat16, (P, H, KV_PAGE)),
-                (v_scale, "v_scale", torch.bfloat16, (P, H, KV_PAGE)),
-                (table, "table", torch.int32, tuple(table.shape)))
-        for t, name, dtype, shape in want:
-            if t.dtype != dtype:
+        P, H, _, d = k.shape
+        B, W = table.shape
+        index = k.get_device()
+        for t, name, dtype, shape in ((k, "k", torch.int8, (P, H, KV_PAGE, d)),
+                                      (v, "v", torch.int8, (P, H, d, KV_PAGE)),
+                                      (k_scale, "k_scale", torch.bfloat16, (P, H, KV_PAGE)),
+                                      (v_scale, "v_scale", torch.bfloat16, (P, H, KV_PAGE)),
+                                      (table, "table", torch.int32, (B, W))):
+            if t.dtype is not dtype:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
             if t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
-            if t.device != dev or not t.is_cuda:
+            if t.get_device() != index or index < 0:
                 raise ValueError(f"{name} is on {t.device}: the cache lives on one CUDA device")
-        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
-        self.device = dev
+        self._k, self._v, self._k_scale, self._v_scale, self._table = k, v, k_scale, v_scale, table
+        self.index, self.batch, self.width, self.kv_heads, self.head_dim = index, B, W, H, d
         self._c = _KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                            table.data_ptr(), P, H, d, table.shape[0], table.shape[1])
+                            table.data_ptr(), P, H, d, B, W)
+        self._ref = ctypes.byref(self._c)
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
+    table = property(lambda self: self._table)
+    device = property(lambda self: self._k.device)
 
     @classmethod
     def zeros(cls, pages: int, kv_heads: int, head_dim: int, table: torch.Tensor):
@@ -478,16 +504,19 @@ def dvssq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: tor
     position start[b] + t - cu[b].  k and v may be slices with any token and
     head strides that are multiples of 8 elements.
     """
-    c = cache._c
-    T = k.shape[0]
-    shape = (T, c.kv_heads, c.head_dim)
-    kp, kt, kh = _rows(k, "k", shape, cache.device)
-    vp, vt, vh = _rows(v, "v", shape, cache.device)
-    sp = _indices(start, "start", c.batch, cache.device)
-    cp = None if cu is None else _indices(cu, "cu", c.batch + 1, cache.device)
-    _launch(cache.device, stream, lambda st: _check(
-        lib.dvssq_kv_append(ctypes.byref(c), kp, kt, kh, vp, vt, vh, T, sp, cp, st),
-        "dvssq_kv_append"))
+    index = cache.index
+    if stream is not None or _current_device() != index:
+        with _on(index, stream):
+            return dvssq_kv_append(cache, k, v, start, cu)
+    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
+    kp, kt, kh = _rows(k, "k", shape, index)
+    vp, vt, vh = _rows(v, "v", shape, index)
+    sp = _indices(start, "start", cache.batch, index)
+    cp = None if cu is None else _indices(cu, "cu", cache.batch + 1, index)
+    s = lib.dvssq_kv_append(cache._ref, kp, kt, kh, vp, vt, vh, shape[0], sp, cp,
+                            _current_stream(index))
+    if s:
+        raise DvssqError(s, "dvssq_kv_append")
 
 
 def dvssq_kv_read(cache: KvCache, start: torch.Tensor, cu: torch.Tensor | None = None,
@@ -499,23 +528,30 @@ def dvssq_kv_read(cache: KvCache, start: torch.Tensor, cu: torch.Tensor | None =
     value, known to the caller) may be left out without ``cu``.  Rows that the
     call does not cover are left as they were (new tensors: undefined).
     """
-    c = cache._c
+    index = cache.index
+    if stream is not None or _current_device() != index:
+        with _on(index, stream):
+            return dvssq_kv_read(cache, start, cu, tokens, k, v)
     if tokens is None:
         if cu is not None:
             raise ValueError("tokens is needed with cu: its last value lives on the device")
-        tokens = c.batch
-    shape = (int(tokens), c.kv_heads, c.head_dim)
-    sp = _indices(start, "start", c.batch, cache.device)
-    cp = None if cu is None else _indices(cu, "cu", c.batch + 1, cache.device)
-
-    def body(st):
-        ko = _result(k, "k", shape, torch.bfloat16, cache.device)
-        vo = _result(v, "v", shape, torch.bfloat16, cache.device)
-        _check(lib.dvssq_kv_read(ctypes.byref(c), ko.data_ptr(), vo.data_ptr(), shape[0], sp, cp, st),
-               "dvssq_kv_read")
-        return ko, vo
-
-    return _launch(cache.device, stream, body)
+        tokens = cache.batch
+    shape = (int(tokens), cache.kv_heads, cache.head_dim)
+    sp = _indices(start, "start", cache.batch, index)
+    cp = None if cu is None else _indices(cu, "cu", cache.batch + 1, index)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache._k.device)
+    else:
+        _given(k, "k", shape, torch.bfloat16, index)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache._k.device)
+    else:
+        _given(v, "v", shape, torch.bfloat16, index)
+    s = lib.dvssq_kv_read(cache._ref, k.data_ptr(), v.data_ptr(), shape[0], sp, cp,
+                          _current_stream(index))
+    if s:
+        raise DvssqError(s, "dvssq_kv_read")
+    return k, v
 
 
 def dvssq_bss_attention_q8_workspace_size(shape: AttnShape) -> int:
@@ -533,43 +569,48 @@ def dvssq_bss_attention_prefix_workspace_size(shape: AttnShape, prefix_len: int)
     return n.value
 
 
-def _attention_q8(where, q, cache, lens, prefix, prefix_len, tau, haze, ctx, out, y_dtype,
-                  workspace, stream):
-    c, dev = cache._c, cache.device
+@functools.lru_cache(maxsize=1024)
+def _attention_q8_shape(batch, q_heads, kv_heads, head_dim, ctx, tau, haze, prefix_len):
+    """The C shape of a call and its workspace bytes (prefix_len -1: the form without a prefix)."""
+    shape = AttnShape(batch, q_heads, kv_heads, head_dim, ctx, tau, haze)
+    if prefix_len < 0:
+        return shape, ctypes.byref(shape), dvssq_bss_attention_q8_workspace_size(shape)
+    return shape, ctypes.byref(shape), dvssq_bss_attention_prefix_workspace_size(shape, prefix_len)
+
+
+def _attention_q8(q, cache, lens, prefix, prefix_len, tau, haze, ctx, out, y_dtype, workspace):
+    index, B, d = cache.index, cache.batch, cache.head_dim
     if q.dim() != 3:
         raise ValueError("q must be [batch][q_heads][head_dim]")
-    Hq = q.shape[1]
-    qp, qb, qh = _rows(q, "q", (c.batch, Hq, c.head_dim), dev)
-    lp = _indices(lens, "lens", c.batch, dev)
-    if y_dtype not in (Y_F32, Y_BF16):
+    rows = (B, q.shape[1], d)
+    qp, qb, qh = _rows(q, "q", rows, index)
+    lp = _indices(lens, "lens", B, index)
+    if y_dtype != Y_F32 and y_dtype != Y_BF16:
         raise ValueError("y_dtype must be Y_F32 or Y_BF16")
     dtype = torch.float32 if y_dtype == Y_F32 else torch.bfloat16
-    shape = AttnShape(c.batch, Hq, c.kv_heads, c.head_dim,
-                      KV_PAGE * c.table_width if ctx is None else int(ctx), tau, haze)
-    if prefix is None:
-        need = dvssq_bss_attention_q8_workspace_size(shape)
+    _, shape, need = _attention_q8_shape(B, rows[1], cache.kv_heads, d,
+                                         KV_PAGE * cache.width if ctx is None else int(ctx), tau, haze,
+                                         -1 if prefix is None else prefix_len)
+    if out is None:
+        out = torch.empty(rows, dtype=dtype, device=cache._k.device)
     else:
-        need = dvssq_bss_attention_prefix_workspace_size(shape, prefix_len)
-
-    def body(st):
-        o = _result(out, "out", (c.batch, Hq, c.head_dim), dtype, dev)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {dev}")
-        nb = ws.numel() * ws.element_size()
-        if prefix is None:
-            s = lib.dvssq_bss_attention_q8(ctypes.byref(shape), ctypes.byref(c), qp, qb, qh, lp,
-                                           o.data_ptr(), y_dtype, ws.data_ptr(), nb, st)
-        else:
-            s = lib.dvssq_bss_attention_prefix(ctypes.byref(shape), ctypes.byref(c), prefix,
-                                               prefix_len, qp, qb, qh, lp, o.data_ptr(), y_dtype,
-                                               ws.data_ptr(), nb, st)
-        _check(s, where)
-        return o
-
-    return _launch(dev, stream, body)
+        _given(out, "out", rows, dtype, index)
+    if workspace is None:
+        workspace, nb = torch.empty(need, dtype=torch.uint8, device=cache._k.device), need
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+        nb = workspace.numel() * workspace.element_size()
+    if prefix is None:
+        s = lib.dvssq_bss_attention_q8(shape, cache._ref, qp, qb, qh, lp, out.data_ptr(), y_dtype,
+                                       workspace.data_ptr(), nb, _current_stream(index))
+    else:
+        s = lib.dvssq_bss_attention_prefix(shape, cache._ref, prefix, prefix_len, qp, qb, qh, lp,
+                                           out.data_ptr(), y_dtype, workspace.data_ptr(), nb,
+                                           _current_stream(index))
+    if s:
+        raise DvssqError(s, "dvssq_bss_attention_q8" if prefix is None else "dvssq_bss_attention_prefix")
+    return out
 
 
 def dvssq_bss_attention_q8(q: torch.Tensor, cache: KvCache, lens: torch.Tensor, tau: float = 1.10,
@@ -581,8 +622,10 @@ def dvssq_bss_attention_q8(q: torch.Tensor, cache: KvCache, lens: torch.Tensor, 
     ``lens`` int32 [B]: each sequence's keys; ``ctx``: an upper bound on them
     (the table's capacity when left out), which sizes the workspace.
     """
-    return _attention_q8("dvssq_bss_attention_q8", q, cache, lens, None, 0, tau, haze, ctx, out,
-                         y_dtype, workspace, stream)
+    if stream is not None or _current_device() != cache.index:
+        with _on(cache.index, stream):
+            return _attention_q8(q, cache, lens, None, 0, tau, haze, ctx, out, y_dtype, workspace)
+    return _attention_q8(q, cache, lens, None, 0, tau, haze, ctx, out, y_dtype, workspace)
 
 
 def dvssq_bss_attention_prefix(q: torch.Tensor, cache: KvCache, lens: torch.Tensor,
@@ -594,9 +637,13 @@ def dvssq_bss_attention_prefix(q: torch.Tensor, cache: KvCache, lens: torch.Tens
     keys in the pages of ``prefix_table`` (int32 [ceil(prefix_len / 64)]); the
     cache's table and ``lens`` describe each sequence's own keys after it."""
     n = int(prefix_len)
-    pp = _indices(prefix_table, "prefix_table", -(-n // KV_PAGE), cache.device)
-    return _attention_q8("dvssq_bss_attention_prefix", q, cache, lens, pp, n, tau, haze, ctx, out,
-                         y_dtype, workspace, stream)
+    if n < 0:
+        raise ValueError("prefix_len must not be negative")
+    pp = _indices(prefix_table, "prefix_table", -(-n // KV_PAGE), cache.index)
+    if stream is not None or _current_device() != cache.index:
+        with _on(cache.index, stream):
+            return _attention_q8(q, cache, lens, pp, n, tau, haze, ctx, out, y_dtype, workspace)
+    return _attention_q8(q, cache, lens, pp, n, tau, haze, ctx, out, y_dtype, workspace)
 
 
 def dvssq_lowrank_workspace_size(M: int, K: int, rank: int) -> int:

@@ -501,7 +501,7 @@ def test_binding_refusals(dv):
         dv.dvssq_bss_attention_q8(q, c, lens, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         dv.dvssq_bss_attention_prefix(q, c, lens, ptable.cuda(), 200)
-    with pytest.raises(dv.DvssqError):
+    with pytest.raises(ValueError):
         dv.dvssq_bss_attention_prefix(q, c, lens, ptable[:0].cuda(), -1)
 
 

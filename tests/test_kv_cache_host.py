@@ -132,19 +132,21 @@ def test_binding_refusals_without_a_gpu(dv):
     with pytest.raises(ValueError):
         dv.KvCache(k[0], k, s, s, table)
     with pytest.raises(TypeError):                                       # indices are int32
-        dv._indices(table.long(), "start", 6, table.device)
+        dv._indices(table.long(), "start", 6, -1)
     with pytest.raises(ValueError):
-        dv._indices(table, "start", 5, table.device)
+        dv._indices(table, "start", 5, -1)
+    with pytest.raises(ValueError, match="cuda:0"):                      # a host tensor beside a CUDA cache
+        dv._indices(table, "start", 6, 0)
     rows = torch.zeros((5, 2, 128), dtype=torch.bfloat16)
-    assert dv._rows(rows, "k", (5, 2, 128), rows.device)[1:] == (256, 128)
+    assert dv._rows(rows, "k", (5, 2, 128), -1)[1:] == (256, 128)
     fused = torch.zeros((5, 8, 128), dtype=torch.bfloat16)[:, 4:6]
-    assert dv._rows(fused, "k", (5, 2, 128), rows.device)[1:] == (1024, 128)
+    assert dv._rows(fused, "k", (5, 2, 128), -1)[1:] == (1024, 128)
     with pytest.raises(TypeError):
-        dv._rows(rows.float(), "k", (5, 2, 128), rows.device)
+        dv._rows(rows.float(), "k", (5, 2, 128), -1)
     with pytest.raises(ValueError):
-        dv._rows(rows, "k", (5, 2, 64), rows.device)
+        dv._rows(rows, "k", (5, 2, 64), -1)
     with pytest.raises(ValueError):
-        dv._rows(torch.zeros((5, 128, 2), dtype=torch.bfloat16).transpose(1, 2), "k", (5, 2, 128), rows.device)
+        dv._rows(torch.zeros((5, 128, 2), dtype=torch.bfloat16).transpose(1, 2), "k", (5, 2, 128), -1)
 
 
 # ----------------------------------------------- pins of the plain implementation
