@@ -35,7 +35,6 @@ namespace dvssq {
 constexpr int kPfxConv = 3;              // converting warpgroups
 constexpr int kPfxThreads = (3 + kPfxConv) * 128;   // two of weights and one that issues beside them
 constexpr int kPfxMma = 4 * (2 + kPfxConv);         // the issuing warp
-constexpr float kLog2e = 1.44269504088896341f;
 
 struct PfxParams {
   Q8Params q8;
@@ -138,12 +137,6 @@ __device__ __forceinline__ void pfx_f16(const uint4 &c, uint4 &lo, uint4 &hi) {
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
-
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // A row's 32 products of half a page: their largest logit over ks (a NaN is passed over).
@@ -339,7 +332,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     const int row = tid & 127, rr = rt * 128 + row;
     const bool live = rr < p.rows;
     const int b = live ? rr / G : 0, hq = h * G + (live ? rr - b * G : 0);
-    const float r1 = s_step[row] * p.q8.scale;       // logit = S ks r1
+    const float r2 = s_step[row] * p.q8.scale2;      // logit (in units of log2 e) = S ks r2
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float mx = -INFINITY, x0 = 0.f, floor2 = -INFINITY;
     float2 sum = make_float2(0.f, 0.f);
@@ -358,11 +351,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         shift = 14 - e;
       }
       if (m > -INFINITY) {
-        x0 = (float)shift - m * kLog2e;              // exponent of a weight: S ks r1 log2e + x0
-        if (p.q8.haze > 0.f) floor2 = (float)shift - p.q8.haze * kLog2e;
+        x0 = (float)shift - m;                       // exponent of a weight: S ks r2 + x0
+        floor2 = (float)shift + p.q8.haze2;
       }
     }
-    const float r2 = r1 * kLog2e;
     for (int j = 0; j < n && ok; ++j) {
       const int sb = j & 3, ss = j % NS;
       const bool got = mbar_wait(&sc_full[sb], (j >> 2) & 1) && mbar_wait(&s_full[ss], (j / NS) & 1);
@@ -400,7 +392,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     }
     if constexpr (!PV) {
       pdl_wait();                                    // the row maxima were cleared by q8_logits
-      const float m = mx * r1;
+      const float m = mx * r2;
       if (live && m == m) atomicMax(&p.mrow[(size_t)b * p.q8.Hq + hq], order_bits(m));
     } else {
       if (!__all_sync(0xffffffffu, ok && mbar_wait(o_full, 0))) ok = false;

@@ -58,7 +58,8 @@ struct Q8Params {
   const float *po, *pl;
   int splits, rows;
   int B, Hq, H, G, W, n_pages, ctx, ctxp, target;
-  float scale, haze;
+  float scale2;                  // tau / sqrt(d) log2 e: logits are held in units of log2 e
+  float haze2;                   // -haze log2 e; -inf: no truncation
 };
 
 // FP32 bits in an order-preserving unsigned form, for an atomic maximum; 0 (no
@@ -78,15 +79,22 @@ __device__ __forceinline__ int q8_len(const Q8Params &p, int b) {
 }
 
 // The plan, the same in every CTA: off[b] = items of the sequences before b (per KV
-// head) in shared memory; returns the pages per item.  N page-heads over r
-// rounds of `target` CTAs, r the fewest whose items stay within kQ8MaxPages.
+// head) in shared memory; returns the pages per item c.  N page-heads over r
+// rounds of `target` CTAs, r the fewest whose items stay within kQ8MaxPages; a
+// sequence's last item may be short, so that there are up to N / c + B H items, and
+// c is chosen for those to fit the rounds (a few items over a round would double
+// the time: 20 us instead of 13 for the logits of 32 sequences of up to 8000 keys).
 __device__ __forceinline__ int q8_plan(const Q8Params &p, int *off) {
   __shared__ int part[kQ8Threads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.B + kQ8Threads - 1) / kQ8Threads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += (q8_len(p, b) + 63) >> 6;
+  for (int b = b0; b < b1; ++b) {
+    const int n = (q8_len(p, b) + 63) >> 6;
+    off[b] = n;                              // this thread's entries: pages first, then offsets
+    sum += n;
+  }
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) part[warp] = sum;
   __syncthreads();
@@ -95,10 +103,11 @@ __device__ __forceinline__ int q8_plan(const Q8Params &p, int *off) {
   for (int i = 0; i < kQ8Threads / 32; ++i) N += part[i];
   N *= p.H;
   const long long round = (long long)p.target * kQ8MaxPages;
-  const long long r = max(1LL, (N + round - 1) / round);
-  const int c = (int)max(1LL, (N + p.target * r - 1) / (p.target * r));
+  const long long slots = p.target * max(1LL, (N + round - 1) / round);
+  const long long room = max(slots - (long long)p.B * p.H, slots - slots / 4);
+  const int c = (int)min((long long)kQ8MaxPages, max(1LL, (N + room - 1) / room));
   int items = 0;
-  for (int b = b0; b < b1; ++b) items += (((q8_len(p, b) + 63) >> 6) + c - 1) / c;
+  for (int b = b0; b < b1; ++b) items += (off[b] + c - 1) / c;
   int scan = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -111,8 +120,9 @@ __device__ __forceinline__ int q8_plan(const Q8Params &p, int *off) {
   int base = scan - items;
   for (int i = 0; i < warp; ++i) base += part[i];
   for (int b = b0; b < b1; ++b) {
+    const int n = (off[b] + c - 1) / c;
     off[b] = base;
-    base += (((q8_len(p, b) + 63) >> 6) + c - 1) / c;
+    base += n;
   }
   if (b1 == p.B && b0 < b1) off[p.B] = base;
   __syncthreads();
@@ -175,36 +185,166 @@ template <int D>
 __device__ __forceinline__ void q8_limbs(const uint16_t *q, int8_t *hi, int8_t *lo, float *step) {
   constexpr int VPL = D / 32;
   const int lane = threadIdx.x & 31;
-  uint32_t bits[VPL], m = 0;
+  const KvRaw<VPL> raw = kv_load<VPL>(q + lane * VPL);
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    bits[i] = q[lane * VPL + i];
-    m = max(m, bits[i] & 0x7FFFu);
-  }
+  for (int i = 0; i < VPL / 2; ++i) m = max(m, max(raw.w[i] & 0x7FFFu, (raw.w[i] >> 16) & 0x7FFFu));
   m = __reduce_max_sync(0xffffffffu, m);
-  const int e = max((int)(m >> 7) - 127, -126);
+  const bool finite = m < 0x7F80u;
+  // times 2^(14 - e) in two exact steps (14 - e is 140 at most)
+  const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100);
+  const float f0 = __int_as_float((up + 127) << 23), f1 = __int_as_float((14 - e - up + 127) << 23);
+  uint32_t ph[(VPL + 3) / 4], pl[(VPL + 3) / 4];
+#pragma unroll
+  for (int i = 0; i < (VPL + 3) / 4; ++i) ph[i] = pl[i] = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
+    const uint32_t bits = i & 1 ? raw.w[i / 2] >> 16 : raw.w[i / 2] & 0xFFFFu;
     // the clamp only meets the mantissa 255/128, one unit above hi = lo = 127
-    const int x = m >= 0x7F80u ? 0 : min(__float2int_rn(ldexpf(bf16_bits_to_f32(bits[i]), 14 - e)), 32639);
+    const int x = finite ? min(__float2int_rn(bf16_bits_to_f32(bits) * f0 * f1), 32639) : 0;
     const int l = ((x + 128) & 255) - 128;
-    lo[lane * VPL + i] = (int8_t)l;
-    hi[lane * VPL + i] = (int8_t)((x - l) >> 8);
+    pl[i / 4] |= ((uint32_t)l & 0xFFu) << (8 * (i & 3));
+    ph[i / 4] |= ((uint32_t)((x - l) >> 8) & 0xFFu) << (8 * (i & 3));
   }
-  if (lane == 0) *step = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, e - 14);
+  kv_store_codes<VPL>(hi + lane * VPL, ph);
+  kv_store_codes<VPL>(lo + lane * VPL, pl);
+  if (lane == 0) *step = finite ? ldexpf(1.0f, e - 14) : __uint_as_float(0x7FC00000u);
+}
+
+// What the two contractions of a run of pages work on, one CTA of four warps.
+template <int D, int NT>
+struct Q8Shared {
+  __align__(16) int8_t limbs[8 * NT][D + 16];
+  float step[4 * NT];
+  float m[4 * NT];                           // maxima of the heads
+  float warp[kQ8Threads / 32][4 * NT];
+  int page[kQ8MaxPages], list[kQ8MaxPages], kept[kQ8MaxPages];
+};
+
+// Page ids of a run's pages [p0, p0 + np) of sequence b; -1 outside the pool.
+__device__ __forceinline__ void q8_pages(const Q8Params &p, int b, int p0, int np, int *page) {
+  if (threadIdx.x < np) {
+    int x = p.table[(size_t)b * p.W + p0 + threadIdx.x];
+    if (x < 0 || x >= p.n_pages) {
+      set_error(kErrBadIndex);
+      x = -1;
+    }
+    page[threadIdx.x] = x;
+  }
+}
+
+// Logits (in units of log2 e) of the run's keys: put(key of the run, head, value), and
+// the maximum per head (lane tig of every quad holds head 4 nt + tig of this
+// warp's keys).  The first pages' rows are on their way before the query is
+// prepared; `fresh`: the query's limbs and fragments are not those held.
+template <int D, int NT, class Put>
+__device__ __forceinline__ void q8_logits_run(const Q8Params &p, Q8Shared<D, NT> &sm, int b, int h,
+                                              int np, int live, bool fresh, uint32_t (&qf)[NT][D / 64][4],
+                                              float (&step)[NT], float (&mx)[NT], Put put) {
+  constexpr int DB = D / 64;                 // 64-byte blocks of a K row
+  constexpr int DEPTH = 8 / DB;              // pages in flight per warp
+  constexpr int GP = 4 * NT;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  // warp w: keys 16 w .. 16 w + 15 of every page
+  const int key = 16 * warp + g;
+  uint4 buf[DEPTH][DB][2];
+  uint16_t sc[DEPTH][2];
+  auto issue = [&](int pp, uint4 (*dst)[2], uint16_t *s) {
+    const size_t ph = (size_t)max(0, sm.page[pp]) * p.H + h;
+    const int8_t *src = p.k + (ph * 64 + key) * D + 16 * tig;
+#pragma unroll
+    for (int j = 0; j < DB; ++j) {
+      dst[j][0] = q8_ldg(src + 64 * j);
+      dst[j][1] = q8_ldg(src + 8 * D + 64 * j);
+    }
+    s[0] = __ldg(p.ks + ph * 64 + key);
+    s[1] = __ldg(p.ks + ph * 64 + key + 8);
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (d < np) issue(d, buf[d], sc[d]);
+  if (fresh) {
+    for (int i = warp; i < GP; i += kQ8Threads / 32) {
+      int8_t *hi = sm.limbs[2 * i], *lo = sm.limbs[2 * i + 1];
+      if (i < p.G) {
+        q8_limbs<D>(p.q + b * p.q_bs + (long long)(h * p.G + i) * p.q_hs, hi, lo, &sm.step[i]);
+      } else {
+        for (int j = lane; j < D; j += 32) hi[j] = lo[j] = 0;
+        if (lane == 0) sm.step[i] = 0.f;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < DB; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(&sm.limbs[8 * nt + g][64 * j + 16 * tig]);
+        qf[nt][j][0] = w.x; qf[nt][j][1] = w.y; qf[nt][j][2] = w.z; qf[nt][j][3] = w.w;
+      }
+      step[nt] = sm.step[4 * nt + tig] * p.scale2;
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) mx[nt] = -INFINITY;
+  for (int pb = 0; pb < np; pb += DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int pp = pb + d;
+      if (pp >= np) break;
+      int acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][i] = 0;
+#pragma unroll
+      for (int j = 0; j < DB; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_s8(acc[nt], word(buf[d][j][0], 2 * s), word(buf[d][j][1], 2 * s),
+                   word(buf[d][j][0], 2 * s + 1), word(buf[d][j][1], 2 * s + 1), qf[nt][j][2 * s],
+                   qf[nt][j][2 * s + 1]);
+      const float k0 = bf16_bits_to_f32(sc[d][0]), k1 = bf16_bits_to_f32(sc[d][1]);
+      const bool ok = sm.page[pp] >= 0;
+      if (pp + DEPTH < np) issue(pp + DEPTH, buf[d], sc[d]);
+      const int at = 64 * pp + key;
+      const bool v0 = ok && at < live, v1 = ok && at + 8 < live;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        // 256 hi + lo in exact integers, rounded once to FP32
+        const float l0 = v0 ? (float)(acc[nt][0] * 256 + acc[nt][1]) * k0 * step[nt] : -INFINITY;
+        const float l1 = v1 ? (float)(acc[nt][2] * 256 + acc[nt][3]) * k1 * step[nt] : -INFINITY;
+        put(at, 4 * nt + tig, l0);
+        put(at + 8, 4 * nt + tig, l1);
+        mx[nt] = fmaxf(mx[nt], fmaxf(l0, l1));
+      }
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], o));
+    if (lane < 4) sm.warp[warp][4 * nt + lane] = mx[nt];
+  }
+  __syncthreads();
+}
+
+// The maximum of head `tid` over the warps of the CTA (tid < 4 NT).
+template <int D, int NT>
+__device__ __forceinline__ float q8_warps_max(const Q8Shared<D, NT> &sm) {
+  float m = sm.warp[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < kQ8Threads / 32; ++w) m = fmaxf(m, sm.warp[w][threadIdx.x]);
+  return m;
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const Q8Params p) {
-  constexpr int DB = D / 64;                 // 64-byte blocks of a K row
-  constexpr int DEPTH = 8 / DB;              // pages in flight per warp
   constexpr int GP = 4 * NT;
   extern __shared__ int off[];
-  __shared__ __align__(16) int8_t limbs[8 * NT][D + 16];
-  __shared__ float s_step[GP];
-  __shared__ float s_max[kQ8Threads / 32][GP];
-  __shared__ int s_page[kQ8MaxPages];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  __shared__ Q8Shared<D, NT> sm;
+  const int tid = threadIdx.x;
   pdl_launch_dependents();
   const int c = q8_plan(p, off);
   if (blockIdx.x == 0)
@@ -215,117 +355,21 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
     for (int i = blockIdx.x * kQ8Threads + tid; i < p.H; i += gridDim.x * kQ8Threads) p.svmax[i] = 0;
   }
   const long long total = (long long)off[p.B] * p.H;
-  int held = -1;                             // the (sequence, KV head) whose limbs are held
-  uint32_t qf[NT][DB][4];
-  float step[NT];
+  int held = -1;                             // the (sequence, KV head) whose query is held
+  uint32_t qf[NT][D / 64][4];
+  float step[NT], mx[NT];
   for (long long item = blockIdx.x; item < total; item += gridDim.x) {
     const int u = (int)(item / p.H), h = (int)(item - (long long)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
     const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
     __syncthreads();                         // the previous item's shared memory is free
-    if (tid < np) {
-      int page = p.table[(size_t)b * p.W + p0 + tid];
-      if (page < 0 || page >= p.n_pages) {
-        set_error(kErrBadIndex);
-        page = -1;
-      }
-      s_page[tid] = page;
-    }
-    const bool fresh = held != b * p.H + h;
-    if (fresh) {
-      for (int i = warp; i < GP; i += kQ8Threads / 32) {
-        int8_t *hi = limbs[2 * i], *lo = limbs[2 * i + 1];
-        if (i < p.G) {
-          q8_limbs<D>(p.q + b * p.q_bs + (long long)(h * p.G + i) * p.q_hs, hi, lo, &s_step[i]);
-        } else {
-          for (int j = lane; j < D; j += 32) hi[j] = lo[j] = 0;
-          if (lane == 0) s_step[i] = 0.f;
-        }
-      }
-      held = b * p.H + h;
-    }
+    q8_pages(p, b, p0, np, sm.page);
     __syncthreads();
-    if (fresh) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int j = 0; j < DB; ++j) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(&limbs[8 * nt + g][64 * j + 16 * tig]);
-          qf[nt][j][0] = w.x; qf[nt][j][1] = w.y; qf[nt][j][2] = w.z; qf[nt][j][3] = w.w;
-        }
-        step[nt] = s_step[4 * nt + tig] * p.scale;
-      }
-    }
-    // warp w: keys 16 w .. 16 w + 15 of every page; DEPTH pages' rows in flight
-    const int key = 16 * warp + g;
-    uint4 buf[DEPTH][DB][2];
-    uint16_t sc[DEPTH][2];
-    auto issue = [&](int pp, uint4 (*dst)[2], uint16_t *s) {
-      const size_t ph = (size_t)max(0, s_page[pp]) * p.H + h;
-      const int8_t *src = p.k + (ph * 64 + key) * D + 16 * tig;
-#pragma unroll
-      for (int j = 0; j < DB; ++j) {
-        dst[j][0] = q8_ldg(src + 64 * j);
-        dst[j][1] = q8_ldg(src + 8 * D + 64 * j);
-      }
-      s[0] = __ldg(p.ks + ph * 64 + key);
-      s[1] = __ldg(p.ks + ph * 64 + key + 8);
-    };
-    float mx[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mx[nt] = -INFINITY;
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (d < np) issue(d, buf[d], sc[d]);
     float *lg = p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0) * GP;
-    for (int pb = 0; pb < np; pb += DEPTH) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        const int pp = pb + d;
-        if (pp >= np) break;
-        int acc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[nt][i] = 0;
-#pragma unroll
-        for (int j = 0; j < DB; ++j)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_s8(acc[nt], word(buf[d][j][0], 2 * s), word(buf[d][j][1], 2 * s),
-                     word(buf[d][j][0], 2 * s + 1), word(buf[d][j][1], 2 * s + 1), qf[nt][j][2 * s],
-                     qf[nt][j][2 * s + 1]);
-        const float k0 = bf16_bits_to_f32(sc[d][0]), k1 = bf16_bits_to_f32(sc[d][1]);
-        const bool ok = s_page[pp] >= 0;
-        if (pp + DEPTH < np) issue(pp + DEPTH, buf[d], sc[d]);
-        const int at = 64 * (p0 + pp) + key;
-        const bool v0 = ok && at < len, v1 = ok && at + 8 < len;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // 256 hi + lo in exact integers, rounded once to FP32
-          const float l0 = v0 ? (float)(acc[nt][0] * 256 + acc[nt][1]) * k0 * step[nt] : -INFINITY;
-          const float l1 = v1 ? (float)(acc[nt][2] * 256 + acc[nt][3]) * k1 * step[nt] : -INFINITY;
-          lg[(64 * pp + key) * GP + 4 * nt + tig] = l0;
-          lg[(64 * pp + key + 8) * GP + 4 * nt + tig] = l1;
-          mx[nt] = fmaxf(mx[nt], fmaxf(l0, l1));
-        }
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], o));
-      if (lane < 4) s_max[warp][4 * nt + lane] = mx[nt];
-    }
-    __syncthreads();
-    if (tid < GP) {
-      float m = s_max[0][tid];
-#pragma unroll
-      for (int w = 1; w < kQ8Threads / 32; ++w) m = fmaxf(m, s_max[w][tid]);
-      p.cmax[item * GP + tid] = m;
-    }
+    q8_logits_run<D, NT>(p, sm, b, h, np, len - 64 * p0, held != b * p.H + h, qf, step, mx,
+                         [&](int key, int head, float v) { lg[key * GP + head] = v; });
+    held = b * p.H + h;
+    if (tid < GP) p.cmax[item * GP + tid] = q8_warps_max(sm);
   }
 }
 
@@ -335,20 +379,179 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
 // odd bytes are then the fragment's pairs.
 constexpr int kQ8WRow = 72;
 
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Weights of the run's keys from its logits (lg [key][4 NT], global or shared) and the
+// final maxima sm.m: two BF16 limbs of exp2(s - m) vs per head, the sums of the
+// exponentials per warp in sm.warp, and the pages that keep a key, in order, in
+// sm.list; returns their number.  Warp w takes pages w, w + 4, ..; a lane two keys
+// of a group of four.  A page whose keys all lie below the threshold costs its
+// logits only.
 template <int D, int NT>
-__global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8Params p) {
+__device__ __forceinline__ int q8_weights_run(const Q8Params &p, Q8Shared<D, NT> &sm,
+                                              uint16_t (*wt)[8 * NT][kQ8WRow], int h, int np,
+                                              const float *lg) {
+  constexpr int GP = 4 * NT, NW = kQ8Threads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float sum[GP], m[GP];
+#pragma unroll
+  for (int i = 0; i < GP; ++i) {
+    sum[i] = 0.f;
+    m[i] = sm.m[i];
+  }
+  const float haze2 = p.haze2;               // -inf where the truncation is off
+  const int key = 4 * (lane >> 1) + (lane & 1);
+  for (int pp = warp; pp < np; pp += NW) {
+    const size_t ph = (size_t)max(0, sm.page[pp]) * p.H + h;
+    float s[2][GP], vs[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float *src = lg + (64 * pp + key + 2 * t) * GP;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float4 f = *reinterpret_cast<const float4 *>(src + 4 * i);
+        s[t][4 * i] = f.x; s[t][4 * i + 1] = f.y; s[t][4 * i + 2] = f.z; s[t][4 * i + 3] = f.w;
+      }
+      vs[t] = bf16_bits_to_f32(p.vs[ph * 64 + key + 2 * t]);
+    }
+    // kept: not a key outside the run (-inf) and not below the threshold; a NaN logit is kept
+    bool any = false;
+    uint32_t keep[2] = {0, 0};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < GP; ++i) {
+        const bool inside = i < p.G && s[t][i] != -INFINITY;
+        s[t][i] -= m[i];
+        keep[t] |= (uint32_t)(inside && !(s[t][i] < haze2)) << i;
+      }
+    any = __any_sync(0xffffffffu, (keep[0] | keep[1]) != 0);
+    if (lane == 0) sm.kept[pp] = any;
+    if (!any) continue;
+#pragma unroll
+    for (int i = 0; i < GP; ++i) {
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        // a dropped key's weight is a zero whatever its scale holds
+        const bool k = keep[t] >> i & 1;
+        const float e = k ? ex2_approx(s[t][i]) : 0.f;
+        sum[i] += e;
+        const float w = k ? e * vs[t] : 0.f;
+        const uint32_t a = f32_to_bf16_rn_bits(w);
+        hi |= a << (16 * t);
+        lo |= (uint32_t)f32_to_bf16_rn_bits(w - bf16_bits_to_f32(a)) << (16 * t);
+      }
+      *reinterpret_cast<uint32_t *>(&wt[pp][2 * i][2 * lane]) = hi;
+      *reinterpret_cast<uint32_t *>(&wt[pp][2 * i + 1][2 * lane]) = lo;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < GP; ++i) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+    if (lane == 0) sm.warp[warp][i] = sum[i];
+  }
+  __syncthreads();
+  const uint32_t mask = __ballot_sync(0xffffffffu, lane < np && sm.kept[lane < np ? lane : 0] != 0);
+  if (warp == 0 && (mask >> lane & 1)) sm.list[__popc(mask & ((1u << lane) - 1))] = lane;
+  __syncthreads();
+  return __popc(mask);
+}
+
+// The sum of the exponentials of head `tid` over the warps of the CTA (tid < 4 NT).
+template <int D, int NT>
+__device__ __forceinline__ float q8_warps_sum(const Q8Shared<D, NT> &sm, int i) {
+  float s = sm.warp[0][i];
+#pragma unroll
+  for (int w = 1; w < kQ8Threads / 32; ++w) s += sm.warp[w][i];
+  return s;
+}
+
+// Sum of the weights times V over the run's n kept pages; put(head, dimension, value)
+// for every head below G.  Warp w: rows (D / 4) w .. of V^T.
+template <int D, int NT, class Put>
+__device__ __forceinline__ void q8_pv_run(const Q8Params &p, Q8Shared<D, NT> &sm,
+                                          const uint16_t (*wt)[8 * NT][kQ8WRow], int h, int n, Put put) {
   constexpr int MT = D / 64;                 // 16-row tiles of V^T per warp
   constexpr int DEPTH = 8 / MT;              // pages in flight per warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.f;
+  const int row = 16 * MT * warp + g;
+  uint4 buf[DEPTH][MT][2];
+  auto issue = [&](int x, uint4 (*dst)[2]) {
+    const size_t ph = (size_t)max(0, sm.page[sm.list[x]]) * p.H + h;
+    const int8_t *src = p.v + (ph * D + row) * 64 + 16 * tig;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      dst[i][0] = q8_ldg(src + 16 * i * 64);
+      dst[i][1] = q8_ldg(src + (16 * i + 8) * 64);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (d < n) issue(d, buf[d]);
+  for (int xb = 0; xb < n; xb += DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int x = xb + d;
+      if (x >= n) break;
+      const uint16_t (*w)[kQ8WRow] = wt[sm.list[x]];
+      uint32_t bw[NT][8];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(&w[8 * nt + g][16 * tig]);
+        const uint4 e = *reinterpret_cast<const uint4 *>(&w[8 * nt + g][16 * tig + 8]);
+        bw[nt][0] = a.x; bw[nt][1] = a.y; bw[nt][2] = a.z; bw[nt][3] = a.w;
+        bw[nt][4] = e.x; bw[nt][5] = e.y; bw[nt][6] = e.z; bw[nt][7] = e.w;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint32_t r0 = word(buf[d][i][0], s), r1 = word(buf[d][i][1], s);
+          const uint32_t a0 = q8_bf16_pair(r0), a2 = q8_bf16_pair(r0 >> 8);
+          const uint32_t a1 = q8_bf16_pair(r1), a3 = q8_bf16_pair(r1 >> 8);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_bf16(acc[i][nt], a0, a1, a2, a3, bw[nt][2 * s], bw[nt][2 * s + 1]);
+        }
+      if (x + DEPTH < n) issue(x + DEPTH, buf[d]);
+    }
+  }
+  // columns 2 tig and 2 tig + 1 are the limbs of one head
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int head = 4 * nt + tig;
+    if (head < p.G) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        put(head, row + 16 * i, acc[i][nt][0] + acc[i][nt][1]);
+        put(head, row + 16 * i + 8, acc[i][nt][2] + acc[i][nt][3]);
+      }
+    }
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8Params p) {
   constexpr int GP = 4 * NT;
-  constexpr int NW = kQ8Threads / 32;
   extern __shared__ __align__(16) uint8_t q8_dsm[];
   uint16_t (*wt)[8 * NT][kQ8WRow] = reinterpret_cast<uint16_t (*)[8 * NT][kQ8WRow]>(q8_dsm);
   int *off = reinterpret_cast<int *>(q8_dsm + sizeof(uint16_t) * kQ8MaxPages * 8 * NT * kQ8WRow);
+  __shared__ Q8Shared<D, NT> sm;
   __shared__ float s_red[kQ8Threads];
-  __shared__ float s_m[GP];
-  __shared__ float s_sum[NW][GP];
-  __shared__ int s_page[kQ8MaxPages], s_list[kQ8MaxPages], s_kept[kQ8MaxPages];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  const int tid = threadIdx.x;
   pdl_launch_dependents();
   const int c = q8_plan(p, off);
   const long long total = (long long)off[p.B] * p.H;
@@ -358,10 +561,7 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
     const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
     __syncthreads();                         // the previous item's shared memory is free
-    if (tid < np) {
-      const int page = p.table[(size_t)b * p.W + p0 + tid];
-      s_page[tid] = page < 0 || page >= p.n_pages ? -1 : page;
-    }
+    q8_pages(p, b, p0, np, sm.page);
     // the final maximum of each head over the sequence's items
     {
       const int i = tid % GP;
@@ -376,137 +576,52 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
       for (int t = tid + GP; t < kQ8Threads; t += GP) m = fmaxf(m, s_red[t]);
       if (p.splits > 0 && tid < p.G)
         m = fmaxf(m, from_order_bits(p.mrow[(size_t)b * p.Hq + h * p.G + tid]));
-      s_m[tid] = m;
+      sm.m[tid] = m;
     }
     __syncthreads();
-    // weights: warp w takes pages w, w + 4, ..; a lane two keys of a group of four
-    {
-      float sum[GP], m[GP], floor_[GP];
-#pragma unroll
-      for (int i = 0; i < GP; ++i) {
-        sum[i] = 0.f;
-        m[i] = s_m[i];
-        floor_[i] = p.haze > 0.f ? m[i] - p.haze : -INFINITY;
-      }
-      const int key = 4 * (lane >> 1) + (lane & 1);
-      const float *lg = p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0 + key) * GP;
-      for (int pp = warp; pp < np; pp += NW) {
-        const size_t ph = (size_t)max(0, s_page[pp]) * p.H + h;
-        float s[2][GP], vs[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const float4 f = *reinterpret_cast<const float4 *>(lg + (64 * pp + 2 * t) * GP + 4 * i);
-            s[t][4 * i] = f.x; s[t][4 * i + 1] = f.y; s[t][4 * i + 2] = f.z; s[t][4 * i + 3] = f.w;
-          }
-          vs[t] = bf16_bits_to_f32(p.vs[ph * 64 + key + 2 * t]);
-        }
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < GP; ++i) {
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            // a dropped key's weight is a zero whatever its scale holds; a NaN logit is kept
-            const bool keep = i < p.G && !(s[t][i] == -INFINITY || s[t][i] < floor_[i]);
-            any |= keep;
-            const float e = keep ? expf(s[t][i] - m[i]) : 0.f;
-            sum[i] += e;
-            const float w = keep ? e * vs[t] : 0.f;
-            const uint32_t a = f32_to_bf16_rn_bits(w);
-            hi |= a << (16 * t);
-            lo |= (uint32_t)f32_to_bf16_rn_bits(w - bf16_bits_to_f32(a)) << (16 * t);
-          }
-          *reinterpret_cast<uint32_t *>(&wt[pp][2 * i][2 * lane]) = hi;
-          *reinterpret_cast<uint32_t *>(&wt[pp][2 * i + 1][2 * lane]) = lo;
-        }
-        any = __any_sync(0xffffffffu, any);
-        if (lane == 0) s_kept[pp] = any;
-      }
-#pragma unroll
-      for (int i = 0; i < GP; ++i) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-        if (lane == 0) s_sum[warp][i] = sum[i];
-      }
-    }
-    __syncthreads();
-    if (tid < GP) {
-      float s = s_sum[0][tid];
-#pragma unroll
-      for (int w = 1; w < NW; ++w) s += s_sum[w][tid];
-      p.psum[item * GP + tid] = s;
-    }
-    // the pages with a weight, in order
-    uint32_t mask = __ballot_sync(0xffffffffu, lane < np && s_kept[lane < np ? lane : 0] != 0);
-    const int n = __popc(mask);
-    if (warp == 0 && (mask >> lane & 1)) s_list[__popc(mask & ((1u << lane) - 1))] = lane;
-    __syncthreads();
-    // warp w: rows (D / 4) w .. of V^T
-    float acc[MT][NT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.f;
-    const int row = 16 * MT * warp + g;
-    uint4 buf[DEPTH][MT][2];
-    auto issue = [&](int x, uint4 (*dst)[2]) {
-      const size_t ph = (size_t)max(0, s_page[s_list[x]]) * p.H + h;
-      const int8_t *src = p.v + (ph * D + row) * 64 + 16 * tig;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        dst[i][0] = q8_ldg(src + 16 * i * 64);
-        dst[i][1] = q8_ldg(src + (16 * i + 8) * 64);
-      }
-    };
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (d < n) issue(d, buf[d]);
-    for (int xb = 0; xb < n; xb += DEPTH) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        const int x = xb + d;
-        if (x >= n) break;
-        const uint16_t (*w)[kQ8WRow] = wt[s_list[x]];
-        uint32_t bw[NT][8];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint4 a = *reinterpret_cast<const uint4 *>(&w[8 * nt + g][16 * tig]);
-          const uint4 e = *reinterpret_cast<const uint4 *>(&w[8 * nt + g][16 * tig + 8]);
-          bw[nt][0] = a.x; bw[nt][1] = a.y; bw[nt][2] = a.z; bw[nt][3] = a.w;
-          bw[nt][4] = e.x; bw[nt][5] = e.y; bw[nt][6] = e.z; bw[nt][7] = e.w;
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint32_t r0 = word(buf[d][i][0], s), r1 = word(buf[d][i][1], s);
-            const uint32_t a0 = q8_bf16_pair(r0), a2 = q8_bf16_pair(r0 >> 8);
-            const uint32_t a1 = q8_bf16_pair(r1), a3 = q8_bf16_pair(r1 >> 8);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(acc[i][nt], a0, a1, a2, a3, bw[nt][2 * s], bw[nt][2 * s + 1]);
-          }
-        if (x + DEPTH < n) issue(x + DEPTH, buf[d]);
-      }
-    }
-    // columns 2 tig and 2 tig + 1 are the limbs of one head
+    const int n = q8_weights_run<D, NT>(p, sm, wt, h, np,
+                                        p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0) * GP);
+    if (tid < GP) p.psum[item * GP + tid] = q8_warps_sum(sm, tid);
     float *dst = p.pacc + item * p.G * D;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int head = 4 * nt + tig;
-      if (head < p.G) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          dst[head * D + row + 16 * i] = acc[i][nt][0] + acc[i][nt][1];
-          dst[head * D + row + 16 * i + 8] = acc[i][nt][2] + acc[i][nt][3];
-        }
-      }
-    }
+    q8_pv_run<D, NT>(p, sm, wt, h, n, [&](int head, int d, float v) { dst[head * D + d] = v; });
   }
+}
+
+// Short contexts (at most kQ8MaxPages pages of table): a CTA takes all keys of one
+// sequence and KV head, keeps their logits in shared memory and writes the
+// output: one launch and no partial sums.
+template <int D, int NT>
+__global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const Q8Params p) {
+  constexpr int GP = 4 * NT;
+  extern __shared__ __align__(16) uint8_t q8_dsm[];
+  const int pages = p.ctxp >> 6;
+  uint16_t (*wt)[8 * NT][kQ8WRow] = reinterpret_cast<uint16_t (*)[8 * NT][kQ8WRow]>(q8_dsm);
+  float *lg = reinterpret_cast<float *>(q8_dsm + sizeof(uint16_t) * pages * 8 * NT * kQ8WRow);
+  __shared__ Q8Shared<D, NT> sm;
+  const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
+  const int len = q8_len(p, b), np = (len + 63) >> 6;
+  const size_t at = ((size_t)b * p.Hq + h * p.G) * D;
+  auto store = [&](int head, int d, float v) {
+    if (p.out_bf16) static_cast<uint16_t *>(p.out)[at + head * D + d] = f32_to_bf16_rn_bits(v);
+    else static_cast<float *>(p.out)[at + head * D + d] = v;
+  };
+  if (np == 0) {                             // no key: zeros
+    for (int i = tid; i < p.G * D; i += kQ8Threads) store(0, i, 0.f);
+    return;
+  }
+  q8_pages(p, b, 0, np, sm.page);
+  __syncthreads();
+  uint32_t qf[NT][D / 64][4];
+  float step[NT], mx[NT];
+  q8_logits_run<D, NT>(p, sm, b, h, np, len, true, qf, step, mx,
+                       [&](int key, int head, float v) { lg[key * GP + head] = v; });
+  if (tid < GP) sm.m[tid] = q8_warps_max(sm);
+  __syncthreads();
+  const int n = q8_weights_run<D, NT>(p, sm, wt, h, np, lg);
+  q8_pv_run<D, NT>(p, sm, wt, h, n, [&](int head, int d, float v) {
+    const float sum = q8_warps_sum(sm, head);
+    store(head, d, sum == 0.f ? 0.f : v / sum);
+  });
 }
 
 // out of one query head: the partials of the sequence's items, then those of the
@@ -589,6 +704,24 @@ size_t q8_pv_smem(int NT, int B) {
   return sizeof(uint16_t) * kQ8MaxPages * 8 * NT * kQ8WRow + (size_t)(B + 1) * 4;
 }
 
+// One CTA per sequence and KV head where its pages fit a CTA's shared memory and
+// either the context is so short that splitting it gains nothing (four pages) or the
+// CTAs fill the SMs anyway.  Measured (16/2 heads of 128, one launch against three):
+// see the launch rule's figures at launch_q8_attention.
+bool q8_is_short(const Q8Shape &s) {
+  const int pages = (s.ctx + 63) / 64;
+  return s.prefix == 0 && pages <= kQ8MaxPages && (pages <= 4 || s.B * s.Hkv >= 2 * kQ8Sms);
+}
+size_t q8_short_smem(int NT, int pages) {
+  return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + 64 * 4 * NT * sizeof(float));
+}
+
+template <int D, int NT>
+cudaError_t q8_run_short(const Q8Params &p, cudaStream_t st, Launcher &L) {
+  return L.launch("q8_short", q8_short_kernel<D, NT>, dim3((unsigned)p.H, (unsigned)p.B),
+                  dim3(kQ8Threads), q8_short_smem(NT, p.ctxp / 64), st, false, p);
+}
+
 template <int D, int NT>
 cudaError_t q8_run(const Q8Params &p, long long items, cudaStream_t st, Launcher &L) {
   const dim3 grid((unsigned)std::min<long long>(items, p.target)), block(kQ8Threads);
@@ -602,7 +735,7 @@ cudaError_t q8_run(const Q8Params &p, long long items, cudaStream_t st, Launcher
 }
 }  // namespace
 
-size_t q8_workspace_bytes(const Q8Shape &s) { return q8_layout(s).total; }
+size_t q8_workspace_bytes(const Q8Shape &s) { return q8_is_short(s) ? 256 : q8_layout(s).total; }
 
 cudaError_t prepare_q8_kernels() {
   cudaError_t e = cudaSuccess;
@@ -611,6 +744,20 @@ cudaError_t prepare_q8_kernels() {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)q8_pv_smem(NT, 4096));
   };
+  auto set_short = [&](const void *k, int NT) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)q8_short_smem(NT, kQ8MaxPages));
+  };
+  set_short((const void *)q8_short_kernel<64, 1>, 1);
+  set_short((const void *)q8_short_kernel<64, 2>, 2);
+  set_short((const void *)q8_short_kernel<64, 4>, 4);
+  set_short((const void *)q8_short_kernel<128, 1>, 1);
+  set_short((const void *)q8_short_kernel<128, 2>, 2);
+  set_short((const void *)q8_short_kernel<128, 4>, 4);
+  set_short((const void *)q8_short_kernel<256, 1>, 1);
+  set_short((const void *)q8_short_kernel<256, 2>, 2);
+  set_short((const void *)q8_short_kernel<256, 4>, 4);
   set((const void *)q8_pv_kernel<64, 1>, 1);
   set((const void *)q8_pv_kernel<64, 2>, 2);
   set((const void *)q8_pv_kernel<64, 4>, 4);
@@ -639,8 +786,8 @@ Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
   p.B = a.s.B; p.Hq = a.s.Hq; p.H = a.s.Hkv; p.G = a.s.Hq / a.s.Hkv; p.W = a.pool.W;
   p.n_pages = a.pool.n_pages; p.ctx = a.s.ctx; p.ctxp = (a.s.ctx + 63) / 64 * 64;
   p.target = y.target;
-  p.scale = a.tau / sqrtf((float)a.s.D);
-  p.haze = a.haze;
+  p.scale2 = (float)((double)a.tau / sqrt((double)a.s.D) * 1.4426950408889634);
+  p.haze2 = a.haze > 0.f ? -a.haze * 1.44269504f : -INFINITY;
   return p;
 }
 }  // namespace
@@ -648,9 +795,11 @@ Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
 cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L) {
   const Q8Layout y = q8_layout(a.s);
   const Q8Params p = q8_params(a, y);
+  const bool once = q8_is_short(a.s);
   const int NT = q8_tiles(p.G);
 #define Q8_CASE(D_, N_) \
-  if (a.s.D == D_ && NT == N_) return q8_run<D_, N_>(p, y.items, st, L);
+  if (a.s.D == D_ && NT == N_)                            \
+    return once ? q8_run_short<D_, N_>(p, st, L) : q8_run<D_, N_>(p, y.items, st, L);
   Q8_CASE(64, 1) Q8_CASE(64, 2) Q8_CASE(64, 4)
   Q8_CASE(128, 1) Q8_CASE(128, 2) Q8_CASE(128, 4)
   Q8_CASE(256, 1) Q8_CASE(256, 2) Q8_CASE(256, 4)

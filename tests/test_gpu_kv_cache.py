@@ -222,6 +222,21 @@ def test_long_ragged_contexts(dv, ctx):
     check(out, P.attention(q, pool, table, lens), DECODE)
 
 
+@pytest.mark.parametrize("Hq,H,d,B,ctx", [(16, 4, 256, 80, 1024), (8, 8, 64, 40, 700), (16, 1, 128, 300, 200),
+                                          (6, 2, 128, 150, 960), (16, 2, 128, 2, 256), (16, 2, 128, 2, 257)])
+def test_short_contexts_in_one_launch(dv, Hq, H, d, B, ctx):
+    """Both sides of the rule that gives a CTA a whole sequence."""
+    lens = [(131 * i + ctx) % (ctx + 1) for i in range(B)]
+    lens[0], lens[1] = ctx, 0
+    q = P.queries(B, Hq, d, seed=B)
+    pool, table, _ = P.filled(B, H, d, lens, seed=ctx, bind=(q, 14.0))
+    c = to_gpu(dv, pool, table)
+    ref = P.attention(q, pool, table, lens)
+    check(dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens), ctx=ctx), ref, DECODE)
+    # the table's capacity, one page more
+    check(dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens)), ref, DECODE)
+
+
 def test_many_short_sequences(dv):
     lens = [(37 * i) % 90 for i in range(600)]
     q = P.queries(600, 4, 64, seed=3)
@@ -270,6 +285,22 @@ def test_extreme_queries_and_keys(dv):
     c = to_gpu(dv, pool, table)
     out = dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens))
     check(out, P.attention(q, pool, table, lens), 5e-4)     # max|q| = 255 beside small values: logits near 60
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 64])
+def test_a_context_of_nan_rows_is_nan(dv, prefix):
+    """Where every key of a sequence reads back as NaN, so does its output."""
+    lens = [1, 3, 0]
+    q = P.queries(3, 4, 64, seed=16)
+    pool, table, ptable = P.filled(3, 2, 64, lens, seed=17, prefix=prefix)
+    pool["ks"][:] = math.nan
+    c = to_gpu(dv, pool, table)
+    if prefix:
+        out = dv.dvssq_bss_attention_prefix(q.cuda(), c, i32(lens), ptable.cuda(), prefix)
+        assert out.isnan().all()
+    else:
+        out = dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens))
+        assert out[:2].isnan().all() and (out[2] == 0).all()
 
 
 def test_nan_rows_reach_only_their_own_head(dv):
@@ -498,7 +529,7 @@ def test_binding_refusals(dv):
     with pytest.raises(dv.DvssqError):
         dv.dvssq_bss_attention_q8(q, c, lens, ctx=10 ** 6)   # longer than the table
     with pytest.raises(dv.DvssqError):
-        dv.dvssq_bss_attention_q8(q, c, lens, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        dv.dvssq_bss_attention_q8(q, c, lens, workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         dv.dvssq_bss_attention_prefix(q, c, lens, ptable.cuda(), 200)
     with pytest.raises(ValueError):
