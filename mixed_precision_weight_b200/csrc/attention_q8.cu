@@ -169,15 +169,6 @@ __device__ __forceinline__ uint32_t word(const uint4 &u, int i) {
   return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
 }
 
-// Bytes 0, 2 (even) or 1, 3 (odd, x already shifted right by 8) of x as a BF16
-// pair: 128 + (low 7 bits), minus 128 or, with the sign bit, 256; all exact.
-__device__ __forceinline__ uint32_t q8_bf16_pair(uint32_t x) {
-  const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, c = (x & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&c));
-  return *reinterpret_cast<const uint32_t *>(&d);
-}
-
 // One query head as limbs: 16-bit integers of step 2^(e - 14), e the exponent of
 // the head's largest magnitude (exact for BF16 values of the top 8 binades,
 // off by at most one unit below); hi and lo rows of bytes.  A whole warp.
@@ -520,8 +511,8 @@ __device__ __forceinline__ void q8_pv_run(const Q8Params &p, Q8Shared<D, NT> &sm
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t r0 = word(buf[d][i][0], s), r1 = word(buf[d][i][1], s);
-          const uint32_t a0 = q8_bf16_pair(r0), a2 = q8_bf16_pair(r0 >> 8);
-          const uint32_t a1 = q8_bf16_pair(r1), a3 = q8_bf16_pair(r1 >> 8);
+          const uint32_t a0 = kv_bf16_pair(r0), a2 = kv_bf16_pair(r0 >> 8);
+          const uint32_t a1 = kv_bf16_pair(r1), a3 = kv_bf16_pair(r1 >> 8);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_bf16(acc[i][nt], a0, a1, a2, a3, bw[nt][2 * s], bw[nt][2 * s + 1]);

@@ -42,26 +42,36 @@ struct KvRun {
 
 // Item -> run.  Sequence b owns the items [cu[b] / 64 + 2 b, cu[b+1] / 64 +
 // 2 (b+1)): n rows touch at most n / 64 + 2 pages, so that range covers them
-// without a prefix sum, and a warp-wide search over cu finds b.  Rows outside
-// [0, T), positions outside the table and pages outside the pool are skipped
-// and flagged.  Whole warps call this; false: nothing to do.
+// without a prefix sum, and a warp-wide search over cu finds b (its last round reads
+// the start positions along, so that a call on up to 31 sequences waits for two
+// loads before its rows: these and the page's id).  Rows outside [0, T), positions
+// outside the table and pages outside the pool are skipped and flagged.  Whole
+// warps call this; false: nothing to do.
 __device__ __forceinline__ bool kv_find_run(const KvIndex &ix, int item, KvRun &r) {
   const int lane = threadIdx.x & 31;
   int b = item, j = 0;
-  long long row0 = item, n = 1;
+  long long row0 = item, n = 1, pos;
   if (ix.cu != nullptr) {
     int lo = 0, hi = ix.B;
-    while (hi - lo > 1) {
+    while (hi - lo > 31) {
       const int step = (hi - lo + 31) / 32, idx = lo + step * (lane + 1);
       const bool le = idx < hi && (ix.cu[idx] >> 6) + 2 * idx <= item;
       lo += step * __popc(__ballot_sync(0xffffffffu, le));
       hi = min(hi, lo + step);
     }
-    b = lo;
-    row0 = ix.cu[b];
-    n = (long long)ix.cu[b + 1] - row0;
+    const int idx = lo + lane;
+    const int first = idx <= ix.B ? ix.cu[idx] : 0, at = idx < ix.B ? ix.start[idx] : 0;
+    const uint32_t le = __ballot_sync(0xffffffffu, idx < hi && (first >> 6) + 2 * idx <= item);
+    const int k = __ffs(~le) - 1;              // candidates before the first that lies behind
+    if (k <= 0) return false;
+    b = lo + k - 1;
+    row0 = __shfl_sync(0xffffffffu, first, k - 1);
+    n = (long long)__shfl_sync(0xffffffffu, first, k) - row0;
+    pos = __shfl_sync(0xffffffffu, at, k - 1);
     j = item - ((int)(row0 >> 6) + 2 * b);
     if (j < 0 || n <= 0) return false;
+  } else {
+    pos = ix.start[b];
   }
   bool bad = false;
   if (row0 < 0 || row0 + n > ix.T) {
@@ -70,7 +80,6 @@ __device__ __forceinline__ bool kv_find_run(const KvIndex &ix, int item, KvRun &
     n = ix.T - row0;
     if (n <= 0) return set_error(kErrBadIndex), false;
   }
-  const long long pos = ix.start[b];
   if (pos < 0) return set_error(kErrBadIndex), false;
   const long long p = (pos >> 6) + j;
   const long long a = max(pos, 64 * p), z = min(pos + n, 64 * (p + 1));
@@ -117,21 +126,13 @@ __device__ __forceinline__ KvRaw<VPL> kv_load(const uint16_t *src) {
   return r;
 }
 
-// x / s rounded to nearest: the reciprocal's quotient with one residual step,
-// exact for these 8-bit significands; the plain division where the residual
-// could fall below the normal range.
-__device__ __forceinline__ int kv_code(float x, float s, float rs, bool plain) {
-  float y;
-  if (plain) {
-    y = __fdiv_rn(x, s);
-  } else {
-    y = x * rs;
-    y = fmaf(fmaf(-y, s, x), rs, y);
-  }
-  return max(-127, min(127, __float2int_rn(y)));
-}
-
 // One row held by a warp -> its scale (BF16 bits) and this lane's VPL codes as bytes.
+// x / s is the reciprocal's quotient with one residual step, exact for these 8-bit
+// significands, and no larger than 127 (1 + 2^-8), so that rounding needs no clamp;
+// adding 1.5 2^23 rounds it to the nearest integer, ties to even, and leaves the
+// code in the low byte.  Two values at a time (packed FP32).  Where the residual
+// could fall below the normal range (s < 1e-27): the plain division, and a clamp,
+// because the scale itself may be a subnormal.
 template <int VPL>
 __device__ __forceinline__ uint32_t kv_quantise(const KvRaw<VPL> &raw, uint32_t *codes) {
   // the largest magnitude by its bits: a NaN or an infinity stays the largest
@@ -146,15 +147,29 @@ __device__ __forceinline__ uint32_t kv_quantise(const KvRaw<VPL> &raw, uint32_t 
   const float s = bf16_bits_to_f32(sb);
 #pragma unroll
   for (int i = 0; i < (VPL + 3) / 4; ++i) codes[i] = 0;
-  if (m < 0x7F80u && sb != 0) {
-    const bool plain = s < 1e-27f;
-    const float rs = plain ? 0.0f : __frcp_rn(s);
+  if (m >= 0x7F80u || sb == 0) return sb;
+  float2 y[VPL / 2];
+  if (s >= 1e-27f) {
+    const float rs = __frcp_rn(s);
+    const float2 r2 = make_float2(rs, rs), n2 = make_float2(-s, -s), magic = make_float2(12582912.0f, 12582912.0f);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const uint32_t h = i & 1 ? raw.w[i / 2] >> 16 : raw.w[i / 2] & 0xFFFFu;
-      const int c = kv_code(bf16_bits_to_f32(h), s, rs, plain);
-      codes[i / 4] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+    for (int i = 0; i < VPL / 2; ++i) {
+      const float2 x = make_float2(__uint_as_float(raw.w[i] << 16), __uint_as_float(raw.w[i] & 0xFFFF0000u));
+      const float2 q = mat_mul2(x, r2);
+      y[i] = mat_add2(mat_fma2(mat_fma2(q, n2, x), r2, q), magic);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL / 2; ++i) {
+      const float a = __fdiv_rn(__uint_as_float(raw.w[i] << 16), s);
+      const float b = __fdiv_rn(__uint_as_float(raw.w[i] & 0xFFFF0000u), s);
+      y[i] = make_float2(fmaxf(-127.f, fminf(127.f, a)) + 12582912.0f, fmaxf(-127.f, fminf(127.f, b)) + 12582912.0f);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL / 2; ++i) {
+    const uint32_t two = __byte_perm(__float_as_uint(y[i].x), __float_as_uint(y[i].y), 0x0040);
+    codes[i / 2] |= i & 1 ? two << 16 : two & 0xFFFFu;
   }
   return sb;
 }
@@ -166,60 +181,86 @@ __device__ __forceinline__ void kv_store_codes(int8_t *dst, const uint32_t *c) {
   else *reinterpret_cast<uint16_t *>(dst) = (uint16_t)c[0];
 }
 
+// 4 x 4 bytes transposed: word i of the result holds byte i of each input word.
+__device__ __forceinline__ void kv_transpose4(const uint32_t a[4], uint32_t o[4]) {
+  const uint32_t x = __byte_perm(a[0], a[1], 0x5140), y = __byte_perm(a[2], a[3], 0x5140);   // bytes 0, 1
+  const uint32_t z = __byte_perm(a[0], a[1], 0x7362), w = __byte_perm(a[2], a[3], 0x7362);   // bytes 2, 3
+  o[0] = __byte_perm(x, y, 0x5410);
+  o[1] = __byte_perm(x, y, 0x7632);
+  o[2] = __byte_perm(z, w, 0x5410);
+  o[3] = __byte_perm(z, w, 0x7632);
+}
+
+// A warp takes aligned groups of four slots, both its groups' rows in flight at
+// once.  A lane then holds the same dimensions of four neighbouring tokens: for V,
+// four-byte words of the transposed page after a byte transposition in registers.
+// They go through shared memory (word w of a row at w ^ (row / VPL mod 16), two-way
+// conflicts at most) so that whole rows of 64 bytes are written.
 template <int D>
 __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvAppendParams p) {
-  constexpr int VPL = D / 32;
-  constexpr int U = 4;                        // rows in flight per warp
-  __shared__ __align__(16) int8_t tile[64][D + 4];
+  constexpr int VPL = D / 32, NC = (VPL + 3) / 4;
+  constexpr int NG = 16 / kKvWarps;           // slot groups per warp
+  __shared__ uint32_t tile[D][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, which = blockIdx.z;
   KvRun r;
   if (!kv_find_run(p.ix, blockIdx.x, r)) return;
-  const uint16_t *src = p.src[which] + r.row0 * p.ts[which] + h * p.hs[which] + lane * VPL;
+  const int s0 = r.slot0, s1 = r.slot0 + r.n;
+  const long long ts = which ? p.ts[1] : p.ts[0], hs = which ? p.hs[1] : p.hs[0];
+  const uint16_t *src = (which ? p.src[1] : p.src[0]) + (r.row0 - s0) * ts + h * hs + lane * VPL;
   const size_t ph = (size_t)r.page * p.H + h;
-  uint16_t *scales = (which ? p.vs : p.ks) + ph * 64 + r.slot0;
-  int8_t *kdst = p.k + (ph * 64 + r.slot0) * D + lane * VPL;
-  for (int i0 = warp; i0 < r.n; i0 += U * kKvWarps) {
-    KvRaw<VPL> raw[U];
+  uint16_t *scales = (which ? p.vs : p.ks) + ph * 64;
+  int8_t *kdst = p.k + ph * 64 * D + lane * VPL;
+  KvRaw<VPL> raw[NG][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u * kKvWarps < r.n)
-        raw[u] = kv_load<VPL>(src + (long long)(i0 + u * kKvWarps) * p.ts[which]);
+  for (int q = 0; q < NG; ++q)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kKvWarps;
-      if (i >= r.n) break;
-      uint32_t codes[(VPL + 3) / 4];
-      const uint32_t sb = kv_quantise<VPL>(raw[u], codes);
-      if (lane == 0) scales[i] = (uint16_t)sb;
-      if (which == 0) kv_store_codes<VPL>(kdst + (size_t)i * D, codes);
-      else if constexpr (VPL == 8) {
-        uint32_t *t = reinterpret_cast<uint32_t *>(&tile[r.slot0 + i][lane * VPL]);
-        t[0] = codes[0];
-        t[1] = codes[1];
+    for (int u = 0; u < 4; ++u) {
+      const int slot = 4 * (warp + kKvWarps * q) + u;
+      if (slot >= s0 && slot < s1) raw[q][u] = kv_load<VPL>(src + slot * ts);
+    }
+#pragma unroll
+  for (int q = 0; q < NG; ++q) {
+    const int w = warp + kKvWarps * q;        // slots 4 w .. 4 w + 3
+    if (4 * w >= s1 || 4 * w + 4 <= s0) continue;
+    uint32_t codes[4][NC];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int slot = 4 * w + u;
+      if (slot >= s0 && slot < s1) {
+        const uint32_t sb = kv_quantise<VPL>(raw[q][u], codes[u]);
+        if (lane == 0) scales[slot] = (uint16_t)sb;
+        if (which == 0) kv_store_codes<VPL>(kdst + (size_t)slot * D, codes[u]);
       } else {
-        kv_store_codes<VPL>(&tile[r.slot0 + i][lane * VPL], codes);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) codes[u][i] = 0;
+      }
+    }
+    if (which == 1) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const uint32_t a[4] = {codes[0][i], codes[1][i], codes[2][i], codes[3][i]};
+        uint32_t o[4];
+        kv_transpose4(a, o);
+#pragma unroll
+        for (int u = 0; u < (VPL < 4 ? VPL : 4); ++u) tile[lane * VPL + 4 * i + u][w ^ (lane & 15)] = o[u];
       }
     }
   }
   if (which == 0) return;
   __syncthreads();
-  // V transposed: word w of dimension dd holds slots 4 w .. 4 w + 3; only the
-  // run's own bytes are written
-  const int s0 = r.slot0, s1 = r.slot0 + r.n;
-  const int w0 = s0 >> 2, nw = ((s1 + 3) >> 2) - w0;
-  int8_t *vdst = p.v + ph * 64 * D;
-  for (int i = tid; i < nw * D; i += kKvThreads) {
-    const int dd = i / nw, w = w0 + i - dd * nw, t0 = 4 * w;
-    int8_t *dst = vdst + dd * 64 + t0;
+  uint32_t *vdst = reinterpret_cast<uint32_t *>(p.v + ph * 64 * D);
+#pragma unroll 4
+  for (int i = tid; i < 16 * D; i += kKvThreads) {
+    const int dd = i >> 4, w = i & 15, t0 = 4 * w;
+    if (t0 >= s1 || t0 + 4 <= s0) continue;
+    const uint32_t x = tile[dd][w ^ ((dd / VPL) & 15)];
     if (t0 >= s0 && t0 + 4 <= s1) {
-      const uint32_t a = (uint8_t)tile[t0][dd], b = (uint8_t)tile[t0 + 1][dd],
-                     c = (uint8_t)tile[t0 + 2][dd], d = (uint8_t)tile[t0 + 3][dd];
-      *reinterpret_cast<uint32_t *>(dst) = a | (b << 8) | (c << 16) | (d << 24);
-    } else {
+      vdst[i] = x;
+    } else {                                  // a run's ragged end: its own bytes only
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (t0 + u >= s0 && t0 + u < s1) dst[u] = tile[t0 + u][dd];
+        if (t0 + u >= s0 && t0 + u < s1) reinterpret_cast<uint8_t *>(vdst + i)[u] = (uint8_t)(x >> (8 * u));
     }
   }
 }
@@ -232,67 +273,95 @@ struct KvReadParams {
   int H;
 };
 
-__device__ __forceinline__ uint32_t kv_value2(int c0, int c1, float s) {
-  return (uint32_t)f32_to_bf16_rn_bits((float)c0 * s) |
-         ((uint32_t)f32_to_bf16_rn_bits((float)c1 * s) << 16);
+// Bytes 0, 2 (even) or 1, 3 (odd, x already shifted right by 8) of x as a BF16
+// pair: 128 + (low 7 bits), minus 128 or, with the sign bit, 256; all exact.
+__device__ __forceinline__ uint32_t kv_bf16_pair(uint32_t x) {
+  const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, c = (x & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&d);
+}
+// Code pair times scale pair: one rounding of the exact product
+__device__ __forceinline__ uint32_t kv_times(uint32_t c, uint32_t s) {
+  const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&c),
+                                   *reinterpret_cast<const __nv_bfloat162 *>(&s));
+  return *reinterpret_cast<const uint32_t *>(&d);
 }
 
+// D threads, four 16-byte pieces of the page each.
+//   K: a piece is 16 dimensions of one row: 32 contiguous bytes out.
+//   V: a warp takes 32 dimensions; a lane 4 of them (one piece each) x 16 tokens, so that
+//      after a transposition of the BF16 results in registers every token's 4
+//      dimensions are 8 contiguous bytes and 8 lanes fill 64.  No shared memory.
 template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadParams p) {
-  constexpr int VPL = D / 32;
-  __shared__ __align__(16) uint32_t tile[D][17];     // V words: slots 4 w .. 4 w + 3 of dimension dd
+__global__ void __launch_bounds__(D) kv_read_kernel(const KvReadParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, which = blockIdx.z;
   KvRun r;
   if (!kv_find_run(p.ix, blockIdx.x, r)) return;
   const size_t ph = (size_t)r.page * p.H + h;
-  uint16_t *dst = p.out[which] + ((size_t)r.row0 * p.H + h) * D;
-  const size_t ts = (size_t)p.H * D;
+  const int s0 = r.slot0, s1 = r.slot0 + r.n;
+  const long long ts = (long long)p.H * D;
+  uint16_t *dst = (which ? p.out[1] : p.out[0]) + (r.row0 - s0) * ts + (long long)h * D;   // slot t at dst + t ts
   if (which == 0) {
-    const int8_t *src = p.k + (ph * 64 + r.slot0) * D + lane * VPL;
-#pragma unroll 4
-    for (int i = warp; i < r.n; i += kKvWarps) {
-      const float s = bf16_bits_to_f32(p.ks[ph * 64 + r.slot0 + i]);
-      uint16_t *o = dst + i * ts + lane * VPL;
-      if constexpr (VPL == 8) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(src + (size_t)i * D));
-        const char4 a = *reinterpret_cast<const char4 *>(&c.x), b = *reinterpret_cast<const char4 *>(&c.y);
-        *reinterpret_cast<uint4 *>(o) = make_uint4(kv_value2(a.x, a.y, s), kv_value2(a.z, a.w, s),
-                                                   kv_value2(b.x, b.y, s), kv_value2(b.z, b.w, s));
-      } else if constexpr (VPL == 4) {
-        const char4 a = __ldg(reinterpret_cast<const char4 *>(src + (size_t)i * D));
-        *reinterpret_cast<uint2 *>(o) = make_uint2(kv_value2(a.x, a.y, s), kv_value2(a.z, a.w, s));
-      } else {
-        const char2 a = __ldg(reinterpret_cast<const char2 *>(src + (size_t)i * D));
-        *reinterpret_cast<uint32_t *>(o) = kv_value2(a.x, a.y, s);
+    constexpr int CPR = D / 16;
+    const int8_t *src = p.k + ph * 64 * D;
+    uint4 c[4];
+    uint32_t s[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int row = (tid + D * x) / CPR;
+      if (row >= s0 && row < s1) {
+        c[x] = __ldg(reinterpret_cast<const uint4 *>(src) + tid + D * x);
+        s[x] = p.ks[ph * 64 + row] * 0x10001u;
       }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int row = (tid + D * x) / CPR, ch = (tid + D * x) % CPR;
+      if (row < s0 || row >= s1) continue;
+      const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t e = kv_times(kv_bf16_pair(w[i]), s[x]), f = kv_times(kv_bf16_pair(w[i] >> 8), s[x]);
+        o[2 * i] = __byte_perm(e, f, 0x5410);
+        o[2 * i + 1] = __byte_perm(e, f, 0x7632);
+      }
+      uint4 *out = reinterpret_cast<uint4 *>(dst + row * ts + 16 * ch);
+      out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      out[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
     return;
   }
-  const int s0 = r.slot0, s1 = r.slot0 + r.n;
-  const int w0 = s0 >> 2, nw = ((s1 + 3) >> 2) - w0;
-  const uint32_t *src = reinterpret_cast<const uint32_t *>(p.v + ph * 64 * D);
-  for (int i = tid; i < nw * D; i += kKvThreads) {
-    const int dd = i / nw, w = i - dd * nw;
-    tile[dd][w] = __ldg(src + dd * 16 + w0 + w);
-  }
-  __syncthreads();
-  // a warp takes four slots at a time, a lane two dimensions of each 64
-  for (int w = warp; w < nw; w += kKvWarps) {
-    const int t0 = 4 * (w0 + w);
-    float s[4];
+  const int d0 = 32 * warp + 4 * (lane >> 2), t0 = 16 * (lane & 3);
+  if (t0 >= s1 || t0 + 16 <= s0) return;
+  uint4 c[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      s[u] = t0 + u >= s0 && t0 + u < s1 ? bf16_bits_to_f32(p.vs[ph * 64 + t0 + u]) : 0.0f;
+  for (int i = 0; i < 4; ++i)
+    c[i] = __ldg(reinterpret_cast<const uint4 *>(p.v + (ph * D + d0 + i) * 64 + t0));
+  const uint4 sa = *reinterpret_cast<const uint4 *>(p.vs + ph * 64 + t0);
+  const uint4 sb = *reinterpret_cast<const uint4 *>(p.vs + ph * 64 + t0 + 8);
+  const uint32_t sc[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const int dd = 64 * j + 2 * lane;
-      const uint32_t a = tile[dd][w], b = tile[dd + 1][w];
+  for (int g = 0; g < 4; ++g) {              // tokens t0 + 4 g .. + 3
+    const uint32_t s02 = __byte_perm(sc[2 * g], sc[2 * g + 1], 0x5410);
+    const uint32_t s13 = __byte_perm(sc[2 * g], sc[2 * g + 1], 0x7632);
+    uint32_t e[4], o[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (t0 + u >= s0 && t0 + u < s1)
-          *reinterpret_cast<uint32_t *>(dst + (size_t)(t0 + u - s0) * ts + dd) =
-              kv_value2((int)(int8_t)(a >> (8 * u)), (int)(int8_t)(b >> (8 * u)), s[u]);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = g == 0 ? c[i].x : g == 1 ? c[i].y : g == 2 ? c[i].z : c[i].w;
+      e[i] = kv_times(kv_bf16_pair(x), s02);       // tokens 0 and 2 of dimension d0 + i
+      o[i] = kv_times(kv_bf16_pair(x >> 8), s13);  // tokens 1 and 3
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + 4 * g + u;
+      if (t < s0 || t >= s1) continue;
+      const uint32_t sel = u < 2 ? 0x5410 : 0x7632;
+      *reinterpret_cast<uint2 *>(dst + t * ts + d0) =
+          u & 1 ? make_uint2(__byte_perm(o[0], o[1], sel), __byte_perm(o[2], o[3], sel))
+                : make_uint2(__byte_perm(e[0], e[1], sel), __byte_perm(e[2], e[3], sel));
     }
   }
 }
@@ -329,7 +398,7 @@ cudaError_t launch_kv_read(const KvPool &c, uint16_t *k, uint16_t *v, long long 
   p.ix = kv_index(c, start, cu, T);
   p.k = c.k; p.v = c.v; p.ks = c.ks; p.vs = c.vs; p.H = c.H;
   p.out[0] = k; p.out[1] = v;
-  const dim3 grid(kv_items(p.ix), (unsigned)c.H, 2), block(kKvThreads);
+  const dim3 grid(kv_items(p.ix), (unsigned)c.H, 2), block((unsigned)c.D);
   if (c.D == 256) return L.launch("kv_read", kv_read_kernel<256>, grid, block, 0, st, false, p);
   if (c.D == 128) return L.launch("kv_read", kv_read_kernel<128>, grid, block, 0, st, false, p);
   return L.launch("kv_read", kv_read_kernel<64>, grid, block, 0, st, false, p);
