@@ -631,8 +631,7 @@ cudaError_t pfx_run(const PfxParams &p, const PfxLayout &y, cudaStream_t st, Lau
   e = L.launch("pfx_pv", pfx_kernel<D, true>, pg, dim3(kPfxThreads), PfxSmem<D, true>::bytes, st,
                true, p);
   if (e != cudaSuccess) return e;
-  return L.launch("q8_merge", q8_merge_kernel<D>, dim3((unsigned)p.q8.Hq, (unsigned)p.q8.B),
-                  dim3(256), 0, st, true, p.q8, 4 * NT);
+  return q8_run_merge<D>(p.q8, 4 * NT, st, L);
 }
 }  // namespace
 

@@ -49,6 +49,7 @@ struct Q8Params {
   void *out;
   int out_bf16;
   float *logit;                  // [B][H][ctxp][4 NT]
+  float *smax;                   // [B][H][pages][4][4 NT]: maxima of each page's 16-key strips
   float *cmax, *psum;            // [items][4 NT]
   float *pacc;                   // [items][G][D]
   int *off;                      // [B + 1] first item of each sequence (per KV head)
@@ -209,8 +210,15 @@ struct Q8Shared {
   float step[4 * NT];
   float m[4 * NT];                           // maxima of the heads
   float warp[kQ8Threads / 32][4 * NT];
-  int page[kQ8MaxPages], list[kQ8MaxPages], kept[kQ8MaxPages];
+  int page[kQ8MaxPages], list[kQ8MaxPages];
+  uint32_t kept;                             // pages with a key above the threshold
 };
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 // Page ids of a run's pages [p0, p0 + np) of sequence b; -1 outside the pool.
 __device__ __forceinline__ void q8_pages(const Q8Params &p, int b, int p0, int np, int *page) {
@@ -224,14 +232,15 @@ __device__ __forceinline__ void q8_pages(const Q8Params &p, int b, int p0, int n
   }
 }
 
-// Logits (in units of log2 e) of the run's keys: put(key of the run, head, value), and
-// the maximum per head (lane tig of every quad holds head 4 nt + tig of this
-// warp's keys).  The first pages' rows are on their way before the query is
+// Logits (in units of log2 e) of the run's keys, put(key of the run, head, value), the
+// maximum of each page's strip of 16 keys, put_max(page, strip, head, value; NaN
+// where the strip has one), and in sm.warp those over the run (NaN passed over).  The
+// first pages' rows are on their way before the query is
 // prepared; `fresh`: the query's limbs and fragments are not those held.
-template <int D, int NT, class Put>
+template <int D, int NT, class Put, class PutMax>
 __device__ __forceinline__ void q8_logits_run(const Q8Params &p, Q8Shared<D, NT> &sm, int b, int h,
                                               int np, int live, bool fresh, uint32_t (&qf)[NT][D / 64][4],
-                                              float (&step)[NT], float (&mx)[NT], Put put) {
+                                              float (&step)[NT], Put put, PutMax put_max) {
   constexpr int DB = D / 64;                 // 64-byte blocks of a K row
   constexpr int DEPTH = 8 / DB;              // pages in flight per warp
   constexpr int GP = 4 * NT;
@@ -275,6 +284,7 @@ __device__ __forceinline__ void q8_logits_run(const Q8Params &p, Q8Shared<D, NT>
       step[nt] = sm.step[4 * nt + tig] * p.scale2;
     }
   }
+  float mx[NT];                              // lane tig of every quad: head 4 nt + tig
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) mx[nt] = -INFINITY;
   for (int pb = 0; pb < np; pb += DEPTH) {
@@ -308,16 +318,17 @@ __device__ __forceinline__ void q8_logits_run(const Q8Params &p, Q8Shared<D, NT>
         const float l1 = v1 ? (float)(acc[nt][2] * 256 + acc[nt][3]) * k1 * step[nt] : -INFINITY;
         put(at, 4 * nt + tig, l0);
         put(at + 8, 4 * nt + tig, l1);
-        mx[nt] = fmaxf(mx[nt], fmaxf(l0, l1));
+        float m = max_nan(l0, l1);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane < 4) put_max(pp, warp, 4 * nt + lane, m);
+        mx[nt] = fmaxf(mx[nt], m);
       }
     }
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], o));
+  for (int nt = 0; nt < NT; ++nt)
     if (lane < 4) sm.warp[warp][4 * nt + lane] = mx[nt];
-  }
   __syncthreads();
 }
 
@@ -348,7 +359,7 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
   const long long total = (long long)off[p.B] * p.H;
   int held = -1;                             // the (sequence, KV head) whose query is held
   uint32_t qf[NT][D / 64][4];
-  float step[NT], mx[NT];
+  float step[NT];
   for (long long item = blockIdx.x; item < total; item += gridDim.x) {
     const int u = (int)(item / p.H), h = (int)(item - (long long)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
@@ -357,8 +368,10 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
     q8_pages(p, b, p0, np, sm.page);
     __syncthreads();
     float *lg = p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0) * GP;
-    q8_logits_run<D, NT>(p, sm, b, h, np, len - 64 * p0, held != b * p.H + h, qf, step, mx,
-                         [&](int key, int head, float v) { lg[key * GP + head] = v; });
+    float *lm = p.smax + ((size_t)(b * p.H + h) * (p.ctxp >> 6) + p0) * 4 * GP;
+    q8_logits_run<D, NT>(p, sm, b, h, np, len - 64 * p0, held != b * p.H + h, qf, step,
+                         [&](int key, int head, float v) { lg[key * GP + head] = v; },
+                         [&](int page, int strip, int head, float v) { lm[(4 * page + strip) * GP + head] = v; });
     held = b * p.H + h;
     if (tid < GP) p.cmax[item * GP + tid] = q8_warps_max(sm);
   }
@@ -376,16 +389,42 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Weights of the run's keys from its logits (lg [key][4 NT], global or shared) and the
-// final maxima sm.m: two BF16 limbs of exp2(s - m) vs per head, the sums of the
-// exponentials per warp in sm.warp, and the pages that keep a key, in order, in
-// sm.list; returns their number.  Warp w takes pages w, w + 4, ..; a lane two keys
-// of a group of four.  A page whose keys all lie below the threshold costs its
-// logits only.
+// What a head's maximum is subtracted as: a sequence without a finite logit subtracts
+// nothing (its NaN logits stay NaN), and the heads that pad a tile lie below every
+// threshold.
+__device__ __forceinline__ float q8_reference(float m, bool padding) {
+  return padding ? INFINITY : m == -INFINITY ? 0.f : m;
+}
+
+// The run's pages with a key at or above the threshold (lm: its strips' maxima, global
+// or shared; references in sm.m), in order, into sm.list; returns their number.
 template <int D, int NT>
-__device__ __forceinline__ int q8_weights_run(const Q8Params &p, Q8Shared<D, NT> &sm,
-                                              uint16_t (*wt)[8 * NT][kQ8WRow], int h, int np,
-                                              const float *lg) {
+__device__ __forceinline__ int q8_kept_pages(const Q8Params &p, Q8Shared<D, NT> &sm, int np, const float *lm) {
+  constexpr int GP = 4 * NT;
+  const int tid = threadIdx.x;
+  if (tid == 0) sm.kept = 0;
+  __syncthreads();
+  uint32_t kept = 0;
+#pragma unroll 4
+  for (int i = tid; i < np * 4 * GP; i += kQ8Threads)
+    if (!(lm[i] - sm.m[i % GP] < p.haze2)) kept |= 1u << (i / (4 * GP));
+  kept = __reduce_or_sync(0xffffffffu, kept);
+  if ((tid & 31) == 0 && kept) atomicOr(&sm.kept, kept);
+  __syncthreads();
+  kept = sm.kept;
+  if (tid < np && (kept >> tid & 1)) sm.list[__popc(kept & ((1u << tid) - 1))] = tid;
+  __syncthreads();
+  return __popc(kept);
+}
+
+// Weights of the n kept pages from the run's logits (lg [key][4 NT], global or shared) and
+// the references sm.m: two BF16 limbs of exp2(s - m) vs per head, and in sm.warp the
+// sums of the exponentials per warp.  Warp w takes kept pages w, w + 4, ..; a lane two
+// keys of a group of four.
+template <int D, int NT>
+__device__ __forceinline__ void q8_weights_run(const Q8Params &p, Q8Shared<D, NT> &sm,
+                                               uint16_t (*wt)[8 * NT][kQ8WRow], int h, int n,
+                                               const float *lg) {
   constexpr int GP = 4 * NT, NW = kQ8Threads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float sum[GP], m[GP];
@@ -396,7 +435,9 @@ __device__ __forceinline__ int q8_weights_run(const Q8Params &p, Q8Shared<D, NT>
   }
   const float haze2 = p.haze2;               // -inf where the truncation is off
   const int key = 4 * (lane >> 1) + (lane & 1);
-  for (int pp = warp; pp < np; pp += NW) {
+#pragma unroll 2
+  for (int x = warp; x < n; x += NW) {
+    const int pp = sm.list[x];
     const size_t ph = (size_t)max(0, sm.page[pp]) * p.H + h;
     float s[2][GP], vs[2];
 #pragma unroll
@@ -405,40 +446,25 @@ __device__ __forceinline__ int q8_weights_run(const Q8Params &p, Q8Shared<D, NT>
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const float4 f = *reinterpret_cast<const float4 *>(src + 4 * i);
-        s[t][4 * i] = f.x; s[t][4 * i + 1] = f.y; s[t][4 * i + 2] = f.z; s[t][4 * i + 3] = f.w;
+        s[t][4 * i] = f.x - m[4 * i]; s[t][4 * i + 1] = f.y - m[4 * i + 1];
+        s[t][4 * i + 2] = f.z - m[4 * i + 2]; s[t][4 * i + 3] = f.w - m[4 * i + 3];
       }
       vs[t] = bf16_bits_to_f32(p.vs[ph * 64 + key + 2 * t]);
     }
-    // kept: not a key outside the run (-inf) and not below the threshold; a NaN logit is kept
-    bool any = false;
-    uint32_t keep[2] = {0, 0};
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < GP; ++i) {
-        const bool inside = i < p.G && s[t][i] != -INFINITY;
-        s[t][i] -= m[i];
-        keep[t] |= (uint32_t)(inside && !(s[t][i] < haze2)) << i;
-      }
-    any = __any_sync(0xffffffffu, (keep[0] | keep[1]) != 0);
-    if (lane == 0) sm.kept[pp] = any;
-    if (!any) continue;
 #pragma unroll
     for (int i = 0; i < GP; ++i) {
-      uint32_t hi = 0, lo = 0;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        // a dropped key's weight is a zero whatever its scale holds
-        const bool k = keep[t] >> i & 1;
-        const float e = k ? ex2_approx(s[t][i]) : 0.f;
-        sum[i] += e;
-        const float w = k ? e * vs[t] : 0.f;
-        const uint32_t a = f32_to_bf16_rn_bits(w);
-        hi |= a << (16 * t);
-        lo |= (uint32_t)f32_to_bf16_rn_bits(w - bf16_bits_to_f32(a)) << (16 * t);
-      }
-      *reinterpret_cast<uint32_t *>(&wt[pp][2 * i][2 * lane]) = hi;
-      *reinterpret_cast<uint32_t *>(&wt[pp][2 * i + 1][2 * lane]) = lo;
+      // (a NaN logit is kept)
+      const float e0 = s[0][i] < haze2 ? 0.f : ex2_approx(s[0][i]);
+      const float e1 = s[1][i] < haze2 ? 0.f : ex2_approx(s[1][i]);
+      sum[i] += e0 + e1;
+      // a key without weight adds nothing whatever its value scale holds
+      const float w0 = e0 == 0.f ? 0.f : e0 * vs[0], w1 = e1 == 0.f ? 0.f : e1 * vs[1];
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(w0, w1);
+      const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hi);
+      const __nv_bfloat162 lo =
+          __floats2bfloat162_rn(w0 - __uint_as_float(hb << 16), w1 - __uint_as_float(hb & 0xFFFF0000u));
+      *reinterpret_cast<uint32_t *>(&wt[x][2 * i][2 * lane]) = hb;
+      *reinterpret_cast<uint32_t *>(&wt[x][2 * i + 1][2 * lane]) = *reinterpret_cast<const uint32_t *>(&lo);
     }
   }
 #pragma unroll
@@ -448,10 +474,6 @@ __device__ __forceinline__ int q8_weights_run(const Q8Params &p, Q8Shared<D, NT>
     if (lane == 0) sm.warp[warp][i] = sum[i];
   }
   __syncthreads();
-  const uint32_t mask = __ballot_sync(0xffffffffu, lane < np && sm.kept[lane < np ? lane : 0] != 0);
-  if (warp == 0 && (mask >> lane & 1)) sm.list[__popc(mask & ((1u << lane) - 1))] = lane;
-  __syncthreads();
-  return __popc(mask);
 }
 
 // The sum of the exponentials of head `tid` over the warps of the CTA (tid < 4 NT).
@@ -464,20 +486,15 @@ __device__ __forceinline__ float q8_warps_sum(const Q8Shared<D, NT> &sm, int i) 
 }
 
 // Sum of the weights times V over the run's n kept pages; put(head, dimension, value)
-// for every head below G.  Warp w: rows (D / 4) w .. of V^T.
+// for every head below G.  Warp w: rows (D / 4) w .. of V^T.  The first pages' rows are
+// on their way before the weights are formed.
 template <int D, int NT, class Put>
 __device__ __forceinline__ void q8_pv_run(const Q8Params &p, Q8Shared<D, NT> &sm,
-                                          const uint16_t (*wt)[8 * NT][kQ8WRow], int h, int n, Put put) {
+                                          uint16_t (*wt)[8 * NT][kQ8WRow], int h, int n, const float *lg,
+                                          Put put) {
   constexpr int MT = D / 64;                 // 16-row tiles of V^T per warp
   constexpr int DEPTH = 8 / MT;              // pages in flight per warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.f;
   const int row = 16 * MT * warp + g;
   uint4 buf[DEPTH][MT][2];
   auto issue = [&](int x, uint4 (*dst)[2]) {
@@ -492,12 +509,20 @@ __device__ __forceinline__ void q8_pv_run(const Q8Params &p, Q8Shared<D, NT> &sm
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d)
     if (d < n) issue(d, buf[d]);
+  q8_weights_run<D, NT>(p, sm, wt, h, n, lg);
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.f;
   for (int xb = 0; xb < n; xb += DEPTH) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       const int x = xb + d;
       if (x >= n) break;
-      const uint16_t (*w)[kQ8WRow] = wt[sm.list[x]];
+      const uint16_t (*w)[kQ8WRow] = wt[x];
       uint32_t bw[NT][8];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -567,14 +592,15 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
       for (int t = tid + GP; t < kQ8Threads; t += GP) m = fmaxf(m, s_red[t]);
       if (p.splits > 0 && tid < p.G)
         m = fmaxf(m, from_order_bits(p.mrow[(size_t)b * p.Hq + h * p.G + tid]));
-      sm.m[tid] = m;
+      sm.m[tid] = q8_reference(m, tid >= p.G);
     }
     __syncthreads();
-    const int n = q8_weights_run<D, NT>(p, sm, wt, h, np,
-                                        p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0) * GP);
-    if (tid < GP) p.psum[item * GP + tid] = q8_warps_sum(sm, tid);
+    const size_t first = (size_t)(b * p.H + h) * p.ctxp + 64 * p0;   // the run's first key
+    const int n = q8_kept_pages<D, NT>(p, sm, np, p.smax + first / 16 * GP);
     float *dst = p.pacc + item * p.G * D;
-    q8_pv_run<D, NT>(p, sm, wt, h, n, [&](int head, int d, float v) { dst[head * D + d] = v; });
+    q8_pv_run<D, NT>(p, sm, wt, h, n, p.logit + first * GP,
+                     [&](int head, int d, float v) { dst[head * D + d] = v; });
+    if (tid < GP) p.psum[item * GP + tid] = q8_warps_sum(sm, tid);
   }
 }
 
@@ -588,6 +614,7 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
   const int pages = p.ctxp >> 6;
   uint16_t (*wt)[8 * NT][kQ8WRow] = reinterpret_cast<uint16_t (*)[8 * NT][kQ8WRow]>(q8_dsm);
   float *lg = reinterpret_cast<float *>(q8_dsm + sizeof(uint16_t) * pages * 8 * NT * kQ8WRow);
+  float *lm = lg + 64 * pages * GP;
   __shared__ Q8Shared<D, NT> sm;
   const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
   const int len = q8_len(p, b), np = (len + 63) >> 6;
@@ -603,13 +630,14 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
   q8_pages(p, b, 0, np, sm.page);
   __syncthreads();
   uint32_t qf[NT][D / 64][4];
-  float step[NT], mx[NT];
-  q8_logits_run<D, NT>(p, sm, b, h, np, len, true, qf, step, mx,
-                       [&](int key, int head, float v) { lg[key * GP + head] = v; });
-  if (tid < GP) sm.m[tid] = q8_warps_max(sm);
+  float step[NT];
+  q8_logits_run<D, NT>(p, sm, b, h, np, len, true, qf, step,
+                       [&](int key, int head, float v) { lg[key * GP + head] = v; },
+                       [&](int page, int strip, int head, float v) { lm[(4 * page + strip) * GP + head] = v; });
+  if (tid < GP) sm.m[tid] = q8_reference(q8_warps_max(sm), tid >= p.G);
   __syncthreads();
-  const int n = q8_weights_run<D, NT>(p, sm, wt, h, np, lg);
-  q8_pv_run<D, NT>(p, sm, wt, h, n, [&](int head, int d, float v) {
+  const int n = q8_kept_pages<D, NT>(p, sm, np, lm);
+  q8_pv_run<D, NT>(p, sm, wt, h, n, lg, [&](int head, int d, float v) {
     const float sum = q8_warps_sum(sm, head);
     store(head, d, sum == 0.f ? 0.f : v / sum);
   });
@@ -618,13 +646,16 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
 // out of one query head: the partials of the sequence's items, then those of the
 // prefix's splits, added in order (thread group j the j-th share of them),
 // divided by the sum of the weights.
-template <int D>
+// NV vectors of 4 dimensions per CTA: 16 where there are few rows (a long axis of
+// partials in 16 shares), else all of them (1024 rows of 256 with 19 partials each: 11 us
+// against 18).
+template <int D, int NV>
 __global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP) {
-  constexpr int NV = D / 4, J = 256 / NV;
+  constexpr int J = 256 / NV;
   __shared__ float4 s_acc[J][NV];
   __shared__ float s_sum[J];
   const int hq = blockIdx.x, b = blockIdx.y, h = hq / p.G, i = hq - h * p.G;
-  const int v = threadIdx.x % NV, j = threadIdx.x / NV;
+  const int v = NV * blockIdx.z + threadIdx.x % NV, j = threadIdx.x / NV;
   pdl_wait();
   const int t0 = p.off[b], own = p.off[b + 1] - t0, nt = own + p.splits;
   const int a = (int)((long long)nt * j / J), z = (int)((long long)nt * (j + 1) / J);
@@ -639,13 +670,13 @@ __global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP)
     sum += t < own ? p.psum[item * GP + i] : p.pl[row];
     acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
   }
-  s_acc[j][v] = acc;
-  if (v == 0) s_sum[j] = sum;
+  s_acc[j][threadIdx.x % NV] = acc;
+  if (threadIdx.x % NV == 0) s_sum[j] = sum;
   __syncthreads();
   if (j != 0) return;
 #pragma unroll
   for (int t = 1; t < J; ++t) {
-    const float4 x = s_acc[t][v];
+    const float4 x = s_acc[t][threadIdx.x];
     acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
     sum += s_sum[t];
   }
@@ -664,7 +695,7 @@ __global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP)
 
 namespace {
 struct Q8Layout {
-  size_t logit, cmax, psum, pacc, off, total;
+  size_t logit, smax, cmax, psum, pacc, off, total;
   int target;
   long long items;               // bound on the items of one call
 };
@@ -683,6 +714,7 @@ Q8Layout q8_layout(const Q8Shape &s) {
     return o;
   };
   y.logit = take((size_t)s.B * s.Hkv * pages * 64 * 4 * NT * 4);
+  y.smax = take((size_t)s.B * s.Hkv * pages * 4 * 4 * NT * 4);
   y.cmax = take((size_t)y.items * 4 * NT * 4);
   y.psum = take((size_t)y.items * 4 * NT * 4);
   y.pacc = take((size_t)y.items * G * s.D * 4);
@@ -704,13 +736,22 @@ bool q8_is_short(const Q8Shape &s) {
   return s.prefix == 0 && pages <= kQ8MaxPages && (pages <= 4 || s.B * s.Hkv >= 2 * kQ8Sms);
 }
 size_t q8_short_smem(int NT, int pages) {
-  return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + 64 * 4 * NT * sizeof(float));
+  return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + (64 + 4) * 4 * NT * sizeof(float));
 }
 
 template <int D, int NT>
 cudaError_t q8_run_short(const Q8Params &p, cudaStream_t st, Launcher &L) {
   return L.launch("q8_short", q8_short_kernel<D, NT>, dim3((unsigned)p.H, (unsigned)p.B),
                   dim3(kQ8Threads), q8_short_smem(NT, p.ctxp / 64), st, false, p);
+}
+
+template <int D>
+cudaError_t q8_run_merge(const Q8Params &p, int GP, cudaStream_t st, Launcher &L) {
+  if (p.B * p.Hq < 2 * kQ8Sms)
+    return L.launch("q8_merge", q8_merge_kernel<D, 16>, dim3((unsigned)p.Hq, (unsigned)p.B, D / 64),
+                    dim3(256), 0, st, true, p, GP);
+  return L.launch("q8_merge", q8_merge_kernel<D, D / 4>, dim3((unsigned)p.Hq, (unsigned)p.B),
+                  dim3(256), 0, st, true, p, GP);
 }
 
 template <int D, int NT>
@@ -721,8 +762,7 @@ cudaError_t q8_run(const Q8Params &p, long long items, cudaStream_t st, Launcher
   if (e != cudaSuccess) return e;
   e = L.launch("q8_pv", q8_pv_kernel<D, NT>, grid, block, q8_pv_smem(NT, p.B), st, true, p);
   if (e != cudaSuccess) return e;
-  return L.launch("q8_merge", q8_merge_kernel<D>, dim3((unsigned)p.Hq, (unsigned)p.B), dim3(256), 0,
-                  st, true, p, 4 * NT);
+  return q8_run_merge<D>(p, 4 * NT, st, L);
 }
 }  // namespace
 
@@ -770,6 +810,7 @@ Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
   p.table = a.pool.table; p.lens = a.lens;
   p.out = a.out; p.out_bf16 = a.out_bf16;
   p.logit = reinterpret_cast<float *>(ws + y.logit);
+  p.smax = reinterpret_cast<float *>(ws + y.smax);
   p.cmax = reinterpret_cast<float *>(ws + y.cmax);
   p.psum = reinterpret_cast<float *>(ws + y.psum);
   p.pacc = reinterpret_cast<float *>(ws + y.pacc);
