@@ -61,6 +61,7 @@ struct Q8Params {
   int B, Hq, H, G, W, n_pages, ctx, ctxp, target;
   float scale2;                  // tau / sqrt(d) log2 e: logits are held in units of log2 e
   float haze2;                   // -haze log2 e; -inf: no truncation
+  KvBits bits;
 };
 
 // FP32 bits in an order-preserving unsigned form, for an atomic maximum; 0 (no
@@ -90,23 +91,23 @@ __device__ __forceinline__ int q8_plan(const Q8Params &p, int *off) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.B + kQ8Threads - 1) / kQ8Threads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int sum = 0;
+  uint32_t sum = 0;
   for (int b = b0; b < b1; ++b) {
     const int n = (q8_len(p, b) + 63) >> 6;
     off[b] = n;                              // this thread's entries: pages first, then offsets
     sum += n;
   }
   sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) part[warp] = sum;
+  if (lane == 0) part[warp] = (int)sum;
   __syncthreads();
-  long long N = 0;
+  uint32_t N = 0;                            // the host bounds it below 2^31
 #pragma unroll
-  for (int i = 0; i < kQ8Threads / 32; ++i) N += part[i];
-  N *= p.H;
-  const long long round = (long long)p.target * kQ8MaxPages;
-  const long long slots = p.target * max(1LL, (N + round - 1) / round);
-  const long long room = max(slots - (long long)p.B * p.H, slots - slots / 4);
-  const int c = (int)min((long long)kQ8MaxPages, max(1LL, (N + room - 1) / room));
+  for (int i = 0; i < kQ8Threads / 32; ++i) N += (uint32_t)part[i];
+  N *= (uint32_t)p.H;
+  const uint32_t round = (uint32_t)p.target * kQ8MaxPages, heads = (uint32_t)p.B * (uint32_t)p.H;
+  const uint32_t slots = p.target * max(1u, (N + round - 1) / round), least = slots - slots / 4;
+  const uint32_t room = slots > heads ? max(slots - heads, least) : least;
+  const int c = (int)min((uint32_t)kQ8MaxPages, max(1u, (N + room - 1) / room));
   int items = 0;
   for (int b = b0; b < b1; ++b) items += (off[b] + c - 1) / c;
   int scan = items;
@@ -356,12 +357,12 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
     for (int i = blockIdx.x * kQ8Threads + tid; i < p.B * p.Hq; i += gridDim.x * kQ8Threads) p.mrow[i] = 0;
     for (int i = blockIdx.x * kQ8Threads + tid; i < p.H; i += gridDim.x * kQ8Threads) p.svmax[i] = 0;
   }
-  const long long total = (long long)off[p.B] * p.H;
+  const uint32_t total = (uint32_t)off[p.B] * (uint32_t)p.H;
   int held = -1;                             // the (sequence, KV head) whose query is held
   uint32_t qf[NT][D / 64][4];
   float step[NT];
-  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
-    const int u = (int)(item / p.H), h = (int)(item - (long long)u * p.H);
+  for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const int u = (int)(item / (uint32_t)p.H), h = (int)(item - (uint32_t)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
     const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
     __syncthreads();                         // the previous item's shared memory is free
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
                          [&](int key, int head, float v) { lg[key * GP + head] = v; },
                          [&](int page, int strip, int head, float v) { lm[(4 * page + strip) * GP + head] = v; });
     held = b * p.H + h;
-    if (tid < GP) p.cmax[item * GP + tid] = q8_warps_max(sm);
+    if (tid < GP) p.cmax[(size_t)item * GP + tid] = q8_warps_max(sm);
   }
 }
 
@@ -495,6 +496,7 @@ __device__ __forceinline__ void q8_pv_run(const Q8Params &p, Q8Shared<D, NT> &sm
   constexpr int MT = D / 64;                 // 16-row tiles of V^T per warp
   constexpr int DEPTH = 8 / MT;              // pages in flight per warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const KvBits bits = p.bits;
   const int row = 16 * MT * warp + g;
   uint4 buf[DEPTH][MT][2];
   auto issue = [&](int x, uint4 (*dst)[2]) {
@@ -536,8 +538,8 @@ __device__ __forceinline__ void q8_pv_run(const Q8Params &p, Q8Shared<D, NT> &sm
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t r0 = word(buf[d][i][0], s), r1 = word(buf[d][i][1], s);
-          const uint32_t a0 = kv_bf16_pair(r0), a2 = kv_bf16_pair(r0 >> 8);
-          const uint32_t a1 = kv_bf16_pair(r1), a3 = kv_bf16_pair(r1 >> 8);
+          const uint32_t a0 = kv_bf16_pair(r0, bits), a2 = kv_bf16_pair(r0 >> 8, bits);
+          const uint32_t a1 = kv_bf16_pair(r1, bits), a3 = kv_bf16_pair(r1 >> 8, bits);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_bf16(acc[i][nt], a0, a1, a2, a3, bw[nt][2 * s], bw[nt][2 * s + 1]);
@@ -570,10 +572,10 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
   const int tid = threadIdx.x;
   pdl_launch_dependents();
   const int c = q8_plan(p, off);
-  const long long total = (long long)off[p.B] * p.H;
+  const uint32_t total = (uint32_t)off[p.B] * (uint32_t)p.H;
   pdl_wait();                                // the logits and maxima of q8_logits
-  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
-    const int u = (int)(item / p.H), h = (int)(item - (long long)u * p.H);
+  for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const int u = (int)(item / (uint32_t)p.H), h = (int)(item - (uint32_t)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
     const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
     __syncthreads();                         // the previous item's shared memory is free
@@ -597,10 +599,10 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
     __syncthreads();
     const size_t first = (size_t)(b * p.H + h) * p.ctxp + 64 * p0;   // the run's first key
     const int n = q8_kept_pages<D, NT>(p, sm, np, p.smax + first / 16 * GP);
-    float *dst = p.pacc + item * p.G * D;
+    float *dst = p.pacc + (size_t)item * p.G * D;
     q8_pv_run<D, NT>(p, sm, wt, h, n, p.logit + first * GP,
                      [&](int head, int d, float v) { dst[head * D + d] = v; });
-    if (tid < GP) p.psum[item * GP + tid] = q8_warps_sum(sm, tid);
+    if (tid < GP) p.psum[(size_t)item * GP + tid] = q8_warps_sum(sm, tid);
   }
 }
 
@@ -819,6 +821,7 @@ Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
   p.n_pages = a.pool.n_pages; p.ctx = a.s.ctx; p.ctxp = (a.s.ctx + 63) / 64 * 64;
   p.target = y.target;
   p.scale2 = (float)((double)a.tau / sqrt((double)a.s.D) * 1.4426950408889634);
+  p.bits = kKvBits;
   p.haze2 = a.haze > 0.f ? -a.haze * 1.44269504f : -INFINITY;
   return p;
 }

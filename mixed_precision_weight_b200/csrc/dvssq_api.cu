@@ -450,6 +450,8 @@ dvssq_status q8_shape(const dvssq_attn_shape *s, int32_t prefix_len, Q8Shape &o)
   if (s->head_dim != 64 && s->head_dim != 128 && s->head_dim != 256)
     return DVSSQ_ERR_UNSUPPORTED_SHAPE;
   if (s->ctx < 1 || s->ctx > (1 << 24) || prefix_len > (1 << 24)) return DVSSQ_ERR_UNSUPPORTED_SHAPE;
+  // the kernels count pages of all sequences and heads in 31 bits
+  if ((int64_t)(s->ctx + 63) / 64 * s->batch * s->kv_heads > INT32_MAX) return DVSSQ_ERR_UNSUPPORTED_SHAPE;
   if (prefix_len < 0) return DVSSQ_ERR_INVALID_ARG;
   if (!(s->tau > 0.f) || s->tau > 1e30f || s->haze != s->haze) return DVSSQ_ERR_INVALID_ARG;
   o.B = s->batch; o.Hq = s->q_heads; o.Hkv = s->kv_heads; o.D = s->head_dim; o.ctx = s->ctx;

@@ -265,27 +265,34 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvAppendPar
   }
 }
 
+// Constants of the code conversion, passed as a kernel parameter: the compiler keeps
+// them in registers, and each mask-and-set below is one instruction (as literals
+// they took two, and the integer pipe bounds the conversion).
+struct KvBits {
+  uint32_t low7, sign, one2, nzero2;
+};
+constexpr KvBits kKvBits = {0x007F007Fu, 0x00800080u, 0x3F803F80u, 0x80008000u};
+
 struct KvReadParams {
   KvIndex ix;
   const int8_t *k, *v;
   const uint16_t *ks, *vs;
   uint16_t *out[2];                // K, V rows [T][H][d]
   int H;
+  KvBits bits;
 };
+
+// a b + c on BF16 pairs, rounded once
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 
 // Bytes 0, 2 (even) or 1, 3 (odd, x already shifted right by 8) of x as a BF16
 // pair: 128 + (low 7 bits), minus 128 or, with the sign bit, 256; all exact.
-__device__ __forceinline__ uint32_t kv_bf16_pair(uint32_t x) {
-  const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, c = (x & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&c));
-  return *reinterpret_cast<const uint32_t *>(&d);
-}
-// Code pair times scale pair: one rounding of the exact product
-__device__ __forceinline__ uint32_t kv_times(uint32_t c, uint32_t s) {
-  const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&c),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&s));
-  return *reinterpret_cast<const uint32_t *>(&d);
+__device__ __forceinline__ uint32_t kv_bf16_pair(uint32_t x, const KvBits &k) {
+  return bf16x2_fma((x & k.low7) | 0x43004300u, k.one2, (x & k.sign) | 0xC300C300u);
 }
 
 // D threads, four 16-byte pieces of the page each.
@@ -301,6 +308,8 @@ __global__ void __launch_bounds__(D) kv_read_kernel(const KvReadParams p) {
   if (!kv_find_run(p.ix, blockIdx.x, r)) return;
   const size_t ph = (size_t)r.page * p.H + h;
   const int s0 = r.slot0, s1 = r.slot0 + r.n;
+  // a code pair times a scale pair: one rounding of the exact product
+  auto times = [&](uint32_t codes, uint32_t s) { return bf16x2_fma(kv_bf16_pair(codes, p.bits), s, p.bits.nzero2); };
   const long long ts = (long long)p.H * D;
   uint16_t *dst = (which ? p.out[1] : p.out[0]) + (r.row0 - s0) * ts + (long long)h * D;   // slot t at dst + t ts
   if (which == 0) {
@@ -324,7 +333,7 @@ __global__ void __launch_bounds__(D) kv_read_kernel(const KvReadParams p) {
       uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t e = kv_times(kv_bf16_pair(w[i]), s[x]), f = kv_times(kv_bf16_pair(w[i] >> 8), s[x]);
+        const uint32_t e = times(w[i], s[x]), f = times(w[i] >> 8, s[x]);
         o[2 * i] = __byte_perm(e, f, 0x5410);
         o[2 * i + 1] = __byte_perm(e, f, 0x7632);
       }
@@ -351,8 +360,8 @@ __global__ void __launch_bounds__(D) kv_read_kernel(const KvReadParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t x = g == 0 ? c[i].x : g == 1 ? c[i].y : g == 2 ? c[i].z : c[i].w;
-      e[i] = kv_times(kv_bf16_pair(x), s02);       // tokens 0 and 2 of dimension d0 + i
-      o[i] = kv_times(kv_bf16_pair(x >> 8), s13);  // tokens 1 and 3
+      e[i] = times(x, s02);       // tokens 0 and 2 of dimension d0 + i
+      o[i] = times(x >> 8, s13);  // tokens 1 and 3
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -398,6 +407,7 @@ cudaError_t launch_kv_read(const KvPool &c, uint16_t *k, uint16_t *v, long long 
   p.ix = kv_index(c, start, cu, T);
   p.k = c.k; p.v = c.v; p.ks = c.ks; p.vs = c.vs; p.H = c.H;
   p.out[0] = k; p.out[1] = v;
+  p.bits = kKvBits;
   const dim3 grid(kv_items(p.ix), (unsigned)c.H, 2), block((unsigned)c.D);
   if (c.D == 256) return L.launch("kv_read", kv_read_kernel<256>, grid, block, 0, st, false, p);
   if (c.D == 128) return L.launch("kv_read", kv_read_kernel<128>, grid, block, 0, st, false, p);

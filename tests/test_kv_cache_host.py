@@ -94,7 +94,8 @@ def test_attention_argument_checks(dv):
                        (A(3, 15, 4, 128, 128, 1.1, 12.0), 2), (A(3, 68, 4, 128, 128, 1.1, 12.0), 2),
                        (A(3, 0, 4, 128, 128, 1.1, 12.0), 2), (A(3, 16, 0, 128, 128, 1.1, 12.0), 2),
                        (A(3, 16, 4, 96, 128, 1.1, 12.0), 2), (A(3, 16, 4, 128, 0, 1.1, 12.0), 2),
-                       (A(3, 16, 4, 128, 2 ** 24 + 1, 1.1, 12.0), 2), (A(3, 16, 4, 128, 128, 0.0, 12.0), 1),
+                       (A(3, 16, 4, 128, 2 ** 24 + 1, 1.1, 12.0), 2), (A(4096, 16, 4, 128, 2 ** 23, 1.1, 12.0), 2),
+                       (A(3, 16, 4, 128, 128, 0.0, 12.0), 1),
                        (A(3, 16, 4, 128, 128, math.nan, 12.0), 1), (A(3, 16, 4, 128, 128, math.inf, 12.0), 1),
                        (A(3, 16, 4, 128, 128, 1.1, math.nan), 1),
                        # not the cache's own shape, or longer than its table
