@@ -44,6 +44,7 @@ struct PfxParams {
   uint32_t *svmax;               // [H] largest finite value scale (bits)
   float *po;                     // [splits][H][rows][D]
   float *pl;                     // [splits][H][rows]
+  uint32_t magic;                // 0x64646464
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
@@ -121,15 +122,16 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
-// 16 codes -> 16 FP16 values in order, as two 16-byte chunks
-__device__ __forceinline__ void pfx_f16(const uint4 &c, uint4 &lo, uint4 &hi) {
+// 16 codes -> 16 FP16 values in order, as two 16-byte chunks.  `magic` is 0x64646464, a
+// kernel parameter: as a literal beside the selector it is not held in a register.
+__device__ __forceinline__ void pfx_f16(const uint4 &c, uint32_t magic, uint4 &lo, uint4 &hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t o[8];
   const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t u = w[i] ^ 0x80808080u;
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    uint32_t a = __byte_perm(u, magic, 0x4140), b = __byte_perm(u, magic, 0x4342);
     const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), bias);
     const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
     o[2 * i] = *reinterpret_cast<const uint32_t *>(&x);
@@ -137,6 +139,20 @@ __device__ __forceinline__ void pfx_f16(const uint4 &c, uint4 &lo, uint4 &hi) {
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// mbar_wait with the limit at hand: read once per thread, because a wait that has to
+// read it wakes up late by that load's latency.
+__device__ __forceinline__ bool pfx_wait(uint64_t *bar, uint32_t parity, long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > limit) {
+      set_error(kErrWaitMbarrier);
+      return false;
+    }
+  }
+  return true;
 }
 
 // A row's 32 products of half a page: their largest logit over ks (a NaN is passed over).
@@ -309,6 +325,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   // tensor memory is held: a dependent grid that wants it may be launched now
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
+  const long long limit = wait_limit();
   bool ok = true;
   if (warp < 4) {
 #pragma unroll 1
@@ -357,7 +374,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     }
     for (int j = 0; j < n && ok; ++j) {
       const int sb = j & 3, ss = j % NS;
-      const bool got = mbar_wait(&sc_full[sb], (j >> 2) & 1) && mbar_wait(&s_full[ss], (j / NS) & 1);
+      const bool got = pfx_wait(&sc_full[sb], (j >> 2) & 1, limit) && pfx_wait(&s_full[ss], (j / NS) & 1, limit);
       // a warp gives up as one: the tensor-memory loads are warp-wide
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       tc_fence_after();
@@ -395,7 +412,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       const float m = mx * r2;
       if (live && m == m) atomicMax(&p.mrow[(size_t)b * p.q8.Hq + hq], order_bits(m));
     } else {
-      if (!__all_sync(0xffffffffu, ok && mbar_wait(o_full, 0))) ok = false;
+      if (!__all_sync(0xffffffffu, ok && pfx_wait(o_full, 0, limit))) ok = false;
       tc_fence_after();
       const float back = ldexpf(1.0f, -shift);
       const size_t at = ((size_t)split * H + h) * p.rows;
@@ -407,7 +424,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       // each warpgroup half of the columns, 32 x 32 blocks through shared memory (the
       // ring, free now): whole 128-byte lines out
       float (*st)[36] = reinterpret_cast<float (*)[36]>(pfx_sm + warp * 32 * 36 * 4);
-      const int sub = lane >> 3, c4 = (lane & 7) * 4;
+      const int sub = lane >> 3, c4 = (lane & 7) * 4, first = rt * 128 + 32 * (warp & 3) + sub;
+      const int rows = ok ? p.rows - first : 0;      // of this lane's rows first + 4 i: those below
+      float *out = p.po + (at + first) * D + c4;
 #pragma unroll 1
       for (int cc = 0; cc < D / 64; ++cc) {
         const int col = wg * (D / 2) + 32 * cc;
@@ -423,10 +442,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int rw = 4 * i + sub, gr = rt * 128 + 32 * (warp & 3) + rw;
-          if (gr < p.rows && ok)
-            *reinterpret_cast<float4 *>(p.po + (at + gr) * D + col + c4) =
-                *reinterpret_cast<const float4 *>(&st[rw][c4]);
+          if (4 * i < rows)
+            *reinterpret_cast<float4 *>(out + 4 * i * D + col) =
+                *reinterpret_cast<const float4 *>(&st[4 * i + sub][c4]);
         }
       }
     }
@@ -435,18 +453,12 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     // --------------------------- codes to FP16 tiles ---------------------------
     const int kt = tid & 127;
     constexpr int NL = D / 32;                       // 16-byte pieces per thread and page
-    constexpr int CPR = D / 16;                      // 16-byte pieces of a K row
-    // K: piece x is in row kr + x (128 / CPR), place ch; FP16 pieces 2 c and 2 c + 1 of the
-    // row; lanes 4-7 store the odd one first, so that eight lanes meet the eight
-    // 16-byte columns
-    const int ch = kt % CPR, kr = kt / CPR, odd = (ch >> 2) & 1;
-    const uint32_t kat = (ch >> 2) * 64 * 128 + kr * 128;
-    const uint32_t k0 = kat + ((((ch & 3) * 2 + odd) ^ (kr & 7)) << 4);
-    const uint32_t k1 = kat + ((((ch & 3) * 2 + 1 - odd) ^ (kr & 7)) << 4);
-    // V: piece x is in row kt / 4 + 32 x
-    const int vr = kt >> 2;
-    const uint32_t v0 = vr * 128 + ((((kt & 3) * 2) ^ (vr & 7)) << 4);
-    const uint32_t v1 = vr * 128 + ((((kt & 3) * 2 + 1) ^ (vr & 7)) << 4);
+    // FP16 pieces 2 c and 2 c + 1 of a tile's row, c = kt mod 4: eight lanes (two rows)
+    // meet the eight 16-byte columns.  K: piece x is in row kt / 4 + 32 (x mod 2) of the
+    // 64-dimension block x / 2; V: in row kt / 4 + 32 x; the same place of the tile.
+    const int rw = kt >> 2;
+    const uint32_t c0 = rw * 128 + ((((kt & 3) * 2) ^ (rw & 7)) << 4);
+    const uint32_t c1 = rw * 128 + ((((kt & 3) * 2 + 1) ^ (rw & 7)) << 4);
     uint32_t svm = 0;
     // a job's codes (and a K page's scales) into registers; page ids one job ahead
     uint4 r[NL];
@@ -463,12 +475,16 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         page = nv = 0;
       }
       const size_t ph = (size_t)page * H + h;
-      const int8_t *src = (k ? p.q8.k : p.q8.v) + ph * 64 * D + kt * 16;
-#pragma unroll
-      for (int x = 0; x < NL; ++x) r[x] = q8_ldg(src + x * 2048);
       if (k) {
+        const int8_t *src = p.q8.k + ph * 64 * D + rw * D + (kt & 3) * 16;
+#pragma unroll
+        for (int x = 0; x < NL; ++x) r[x] = q8_ldg(src + (x & 1) * 32 * D + (x >> 1) * 64);
         ks = p.q8.ks[ph * 64 + (kt & 63)];
         vs = p.q8.vs[ph * 64 + (kt & 63)];
+      } else {
+        const int8_t *src = p.q8.v + ph * 64 * D + kt * 16;
+#pragma unroll
+        for (int x = 0; x < NL; ++x) r[x] = q8_ldg(src + x * 2048);
       }
     };
     int t = wg - 2;
@@ -478,20 +494,19 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       const int slot = t % R, j = page_of(t), sb = j & 3;
       const bool k = is_k(t);
       bool got = true;
-      if (t >= R) got = mbar_wait(&empty[slot], ((t / R) - 1) & 1);
+      if (t >= R) got = pfx_wait(&empty[slot], ((t / R) - 1) & 1, limit);
       // the weights of page j - 4 are done with this slot of scales
-      if (k && j >= 4) got = got && mbar_wait(&s_empty[sb], ((j >> 2) - 1) & 1);
+      if (k && j >= 4) got = got && pfx_wait(&s_empty[sb], ((j >> 2) - 1) & 1, limit);
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
       uint8_t *dst = pfx_sm + slot * L::kSlot;
-      if (k) {
 #pragma unroll
-        for (int x = 0; x < NL; ++x) {
-          uint4 lo, hi;
-          pfx_f16(r[x], lo, hi);
-          const int o = x * (128 / CPR) * 128;
-          *reinterpret_cast<uint4 *>(dst + k0 + o) = odd ? hi : lo;
-          *reinterpret_cast<uint4 *>(dst + k1 + o) = odd ? lo : hi;
-        }
+      for (int x = 0; x < NL; ++x) {
+        uint4 lo, hi;
+        pfx_f16(r[x], p.magic, lo, hi);
+        *reinterpret_cast<uint4 *>(dst + c0 + x * 32 * 128) = lo;
+        *reinterpret_cast<uint4 *>(dst + c1 + x * 32 * 128) = hi;
+      }
+      if (k) {
         if ((kt & 63) < nv && vs < 0x7F80u) svm = max(svm, vs);
         const bool nan = __any_sync(0xffffffffu, vs >= 0x7F80u);
         if (kt < 64) {
@@ -500,14 +515,6 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         }
         if (kt == 0) s_nv[sb][0] = nv;
         if (kt == 0 || kt == 32) reinterpret_cast<uint16_t *>(&s_nv[sb][1])[kt >> 5] = nan;
-      } else {
-#pragma unroll
-        for (int x = 0; x < NL; ++x) {
-          uint4 lo, hi;
-          pfx_f16(r[x], lo, hi);
-          *reinterpret_cast<uint4 *>(dst + v0 + x * 32 * 128) = lo;
-          *reinterpret_cast<uint4 *>(dst + v1 + x * 32 * 128) = hi;
-        }
       }
       if (t + kPfxConv < jobs) fetch(t + kPfxConv);
       fence_proxy_async_smem();
@@ -536,12 +543,12 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       };
       auto qk = [&](int j) {
         const int ss = j % NS;
-        bool got = mbar_wait(&full[slot], par);
-        if (!PV && j >= NS) got = got && mbar_wait(&s_empty[ss], ((j / NS) - 1) & 1);
+        bool got = pfx_wait(&full[slot], par, limit);
+        if (!PV && j >= NS) got = got && pfx_wait(&s_empty[ss], ((j / NS) - 1) & 1, limit);
         // S j - 2 holds the weights of w V j - 2: that product has to be done
         if (PV && j >= 2) {
           const int tv = 2 * (j - 1);                // its V's job
-          got = got && mbar_wait(&empty[tv % R], (tv / R) & 1);
+          got = got && pfx_wait(&empty[tv % R], (tv / R) & 1, limit);
         }
         if (!__all_sync(0xffffffffu, got)) return false;
         tc_fence_after();
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       };
       auto wv = [&](int j) {
         const int ss = j % NS;
-        const bool got = mbar_wait(&w_full[ss], (j / NS) & 1) && mbar_wait(&full[slot], par);
+        const bool got = pfx_wait(&w_full[ss], (j / NS) & 1, limit) && pfx_wait(&full[slot], par, limit);
         if (!__all_sync(0xffffffffu, got)) return false;
         tc_fence_after();
         const uint64_t vb = desc + (uint64_t)(slot * (L::kSlot >> 4));
@@ -657,6 +664,7 @@ cudaError_t launch_prefix_attention(const Q8Args &a, cudaStream_t st, Launcher &
   PfxParams p{};
   p.q8 = q8_params(a, y.q8);
   p.ptable = a.ptable;
+  p.magic = 0x64646464u;
   p.prefix = a.s.prefix; p.pages = y.pages; p.splits = y.splits; p.rows = y.rows;
   p.mrow = reinterpret_cast<uint32_t *>(ws + y.mrow);
   p.svmax = reinterpret_cast<uint32_t *>(ws + y.svmax);
