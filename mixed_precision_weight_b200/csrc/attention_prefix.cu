@@ -4,10 +4,10 @@
 // of dense products instead of B walks over it:
 //   S = Q K^T,   w = exp(S - m) vs (zero below the haze threshold),   O = w V
 // The haze threshold needs each row's final maximum first, so Q K^T runs twice:
-//   pfx_max   S and its row maxima (an atomic maximum: any order, one result),
-//             and the largest value scale of each KV head
+//   pfx_max   S and each split's row maxima, and its largest value scale per KV head
 //   pfx_pv    S again (K comes from L2 now), the weights, and a split's O
-// Each sequence's own keys go through q8_logits and q8_pv as without a prefix,
+// Each sequence's own keys go through q8_short, or q8_logits and q8_pv, as without a
+// prefix; those form the maxima over prefix and own keys between the two passes,
 // and q8_merge adds the items' and the splits' partials in order.
 //
 // A CTA holds 128 rows of Q and walks a split of the prefix page by page (64
@@ -40,8 +40,8 @@ struct PfxParams {
   Q8Params q8;
   const int32_t *ptable;
   int prefix, pages, splits, rows;          // rows = B G per KV head
-  uint32_t *mrow;                // [B][Hq] row maxima, order-preserving bits
-  uint32_t *svmax;               // [H] largest finite value scale (bits)
+  float *pmax;                   // [splits][H][rows] row maxima
+  float *psv;                    // [splits][H] largest finite value scales
   float *po;                     // [splits][H][rows][D]
   float *pl;                     // [splits][H][rows]
   uint32_t magic;                // 0x64646464
@@ -227,7 +227,8 @@ struct PfxSmem {
   static constexpr int sv = sa + 4 * 64 * 4;             // float [4][64]: value scales
   static constexpr int step = sv + 4 * 64 * 4;           // float [128]
   static constexpr int nv = step + 128 * 4;              // int [4][2]: live keys, NaN value scales
-  static constexpr int bar = nv + 32;
+  static constexpr int svm = nv + 32;                    // uint32 [12]: largest value scales of the converting warps
+  static constexpr int bar = svm + 48;
   static constexpr int bytes = bar + (2 * R + 15) * 8 + 16;
   static_assert(128 * kQRow <= R * kSlot && 8 * 32 * 36 * 4 <= R * kSlot, "staging fits the ring");
   static_assert(bytes <= 232448, "shared memory of one CTA");
@@ -249,6 +250,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   float (*s_a)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sa);
   float (*s_v)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sv);
   float *s_step = reinterpret_cast<float *>(pfx_sm + L::step);
+  uint32_t *s_svm = reinterpret_cast<uint32_t *>(pfx_sm + L::svm);
   int (*s_nv)[2] = reinterpret_cast<int (*)[2]>(pfx_sm + L::nv);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
   const int split = blockIdx.x, h = blockIdx.y, rt = blockIdx.z;
@@ -355,16 +357,13 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     float2 sum = make_float2(0.f, 0.f);
     int shift = 0;
     if constexpr (PV) {
-      pdl_wait();                                    // the row maxima, of the prefix and of the items
-      float m = from_order_bits(*(volatile uint32_t *)&p.mrow[(size_t)b * p.q8.Hq + hq]);
-      const int gp = 4 * q8_tiles(G);
-      for (int t = p.q8.off[b]; t < p.q8.off[b + 1]; ++t)
-        m = fmaxf(m, p.q8.cmax[((long long)t * H + h) * gp + hq - h * G]);
+      pdl_wait();                                    // the row maxima, over the prefix and the own keys
+      const float m = *(volatile float *)&p.q8.mfin[(size_t)b * p.q8.Hq + hq];
       // weights times 2^shift: the largest vs 2^shift lies in [2^13, 2^14)
-      const uint32_t sv = p.svmax[h];
-      if (sv != 0) {
+      const float sv = *(volatile float *)&p.q8.svfin[h];
+      if (sv > 0.f) {
         int e;
-        frexpf(__uint_as_float(sv), &e);             // vs < 2^e
+        frexpf(sv, &e);                              // vs < 2^e
         shift = 14 - e;
       }
       if (m > -INFINITY) {
@@ -408,9 +407,11 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     }
     if constexpr (!PV) {
-      pdl_wait();                                    // the row maxima were cleared by q8_logits
-      const float m = mx * r2;
-      if (live && m == m) atomicMax(&p.mrow[(size_t)b * p.q8.Hq + hq], order_bits(m));
+      // the two warpgroups' halves of the row (every thread has read its step: all S are done)
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (wg == 1) s_step[row] = mx;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (wg == 0 && live) p.pmax[((size_t)split * H + h) * p.rows + rr] = fmaxf(mx, s_step[row]) * r2;
     } else {
       if (!__all_sync(0xffffffffu, ok && pfx_wait(o_full, 0, limit))) ok = false;
       tc_fence_after();
@@ -525,10 +526,15 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       }
     }
     if constexpr (!PV) {
-      pdl_wait();                                    // svmax was cleared by q8_logits
+      // over the converting warpgroups
       __syncwarp();
       svm = __reduce_max_sync(0xffffffffu, svm);
-      if (lane == 0 && svm != 0) atomicMax(&p.svmax[h], svm << 16);
+      if (lane == 0) s_svm[warp - 8] = svm;
+      asm volatile("bar.sync 2, %0;" ::"n"(kPfxConv * 128) : "memory");
+      if (tid == 256 && rt == 0) {
+        for (int i = 1; i < 4 * kPfxConv; ++i) svm = max(svm, s_svm[i]);
+        p.psv[(size_t)split * H + h] = bf16_bits_to_f32(svm);
+      }
     }
   } else {
     if (warp == kPfxMma) {
@@ -587,6 +593,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       if constexpr (PV) tc_commit_lead(lead, o_full);
     }
   }
+  // what follows waits for this grid only: it ends after the one before it
+  if constexpr (!PV) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kPfxMma) {
@@ -598,7 +606,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
 namespace {
 struct PfxLayout {
   Q8Layout q8;
-  size_t mrow, svmax, po, pl, total;
+  size_t pmax, psv, mfin, svfin, po, pl, total;
   int pages, splits, rows, row_tiles;
 };
 PfxLayout pfx_layout(const Q8Shape &s) {
@@ -615,8 +623,10 @@ PfxLayout pfx_layout(const Q8Shape &s) {
     at += (bytes + 255) & ~(size_t)255;
     return o;
   };
-  y.mrow = take((size_t)s.B * s.Hq * 4);
-  y.svmax = take((size_t)s.Hkv * 4);
+  y.pmax = take((size_t)y.splits * s.Hkv * y.rows * 4);
+  y.psv = take((size_t)y.splits * s.Hkv * 4);
+  y.mfin = take((size_t)s.B * s.Hq * 4);
+  y.svfin = take((size_t)s.Hkv * 4);
   y.po = take((size_t)y.splits * s.Hkv * y.rows * s.D * 4);
   y.pl = take((size_t)y.splits * s.Hkv * y.rows * 4);
   y.total = at;
@@ -625,15 +635,21 @@ PfxLayout pfx_layout(const Q8Shape &s) {
 
 template <int D, int NT>
 cudaError_t pfx_run(const PfxParams &p, const PfxLayout &y, cudaStream_t st, Launcher &L) {
+  // The first launch waits for the stream; the later ones are programmatic dependents.
+  // Each waits for its predecessor before it ends, so that one wait covers all before.
   const dim3 block(kQ8Threads), grid((unsigned)std::min<long long>(y.q8.items, p.q8.target));
   const dim3 pg((unsigned)y.splits, (unsigned)p.q8.H, (unsigned)y.row_tiles);
-  cudaError_t e = L.launch("q8_logits", q8_logits_kernel<D, NT>, grid, block,
-                           (size_t)(p.q8.B + 1) * 4, st, false, p.q8);
+  const bool once = p.q8.single;
+  cudaError_t e = cudaSuccess;
+  if (!once)
+    e = L.launch("q8_logits", q8_logits_kernel<D, NT>, grid, block, (size_t)(p.q8.B + 1) * 4, st,
+                 false, p.q8);
   if (e != cudaSuccess) return e;
   e = L.launch("pfx_max", pfx_kernel<D, false>, pg, dim3(kPfxThreads), PfxSmem<D, false>::bytes, st,
-               true, p);
+               !once, p);
   if (e != cudaSuccess) return e;
-  e = L.launch("q8_pv", q8_pv_kernel<D, NT>, grid, block, q8_pv_smem(NT, p.q8.B), st, true, p.q8);
+  e = once ? q8_run_short<D, NT>(p.q8, st, L)
+           : L.launch("q8_pv", q8_pv_kernel<D, NT>, grid, block, q8_pv_smem(NT, p.q8.B), st, true, p.q8);
   if (e != cudaSuccess) return e;
   e = L.launch("pfx_pv", pfx_kernel<D, true>, pg, dim3(kPfxThreads), PfxSmem<D, true>::bytes, st,
                true, p);
@@ -666,12 +682,15 @@ cudaError_t launch_prefix_attention(const Q8Args &a, cudaStream_t st, Launcher &
   p.ptable = a.ptable;
   p.magic = 0x64646464u;
   p.prefix = a.s.prefix; p.pages = y.pages; p.splits = y.splits; p.rows = y.rows;
-  p.mrow = reinterpret_cast<uint32_t *>(ws + y.mrow);
-  p.svmax = reinterpret_cast<uint32_t *>(ws + y.svmax);
+  p.pmax = reinterpret_cast<float *>(ws + y.pmax);
+  p.psv = reinterpret_cast<float *>(ws + y.psv);
   p.po = reinterpret_cast<float *>(ws + y.po);
   p.pl = reinterpret_cast<float *>(ws + y.pl);
-  p.q8.mrow = p.mrow; p.q8.svmax = p.svmax; p.q8.po = p.po; p.q8.pl = p.pl;
+  p.q8.pmax = p.pmax; p.q8.psv = p.psv; p.q8.po = p.po; p.q8.pl = p.pl;
+  p.q8.mfin = reinterpret_cast<float *>(ws + y.mfin);
+  p.q8.svfin = reinterpret_cast<float *>(ws + y.svfin);
   p.q8.splits = y.splits; p.q8.rows = y.rows;
+  p.q8.single = q8_is_short(a.s);
   const int NT = q8_tiles(p.q8.G);
 #define PFX_CASE(D_, N_) \
   if (a.s.D == D_ && NT == N_) return pfx_run<D_, N_>(p, y, st, L);

@@ -53,26 +53,19 @@ struct Q8Params {
   float *cmax, *psum;            // [items][4 NT]
   float *pacc;                   // [items][G][D]
   int *off;                      // [B + 1] first item of each sequence (per KV head)
-  // a shared prefix (splits > 0): its row maxima, its largest value scale per KV
-  // head, and its splits' partial sums, rows = B G per KV head
-  uint32_t *mrow, *svmax;
+  // a shared prefix (splits > 0), rows = B G per KV head: every split's row maxima
+  // [splits][H][rows] and largest value scale [splits][H], their maxima with the own
+  // keys' [B][Hq] and [H], which this part's kernels write, and the splits' partial sums
+  const float *pmax, *psv;
+  float *mfin, *svfin;
   const float *po, *pl;
   int splits, rows;
+  int single;                    // one item per sequence and KV head, whatever its length
   int B, Hq, H, G, W, n_pages, ctx, ctxp, target;
   float scale2;                  // tau / sqrt(d) log2 e: logits are held in units of log2 e
   float haze2;                   // -haze log2 e; -inf: no truncation
   KvBits bits;
 };
-
-// FP32 bits in an order-preserving unsigned form, for an atomic maximum; 0 (no
-// value's form) reads as -inf.
-__device__ __forceinline__ uint32_t order_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float from_order_bits(uint32_t u) {
-  return u == 0 ? -INFINITY : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
-}
 
 __device__ __forceinline__ int q8_len(const Q8Params &p, int b) {
   const int n = p.lens[b];
@@ -352,11 +345,6 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
   const int c = q8_plan(p, off);
   if (blockIdx.x == 0)
     for (int b = tid; b <= p.B; b += kQ8Threads) p.off[b] = off[b];
-  if (p.splits > 0) {
-    // the prefix kernels raise these by atomic maxima (0 lies below every value)
-    for (int i = blockIdx.x * kQ8Threads + tid; i < p.B * p.Hq; i += gridDim.x * kQ8Threads) p.mrow[i] = 0;
-    for (int i = blockIdx.x * kQ8Threads + tid; i < p.H; i += gridDim.x * kQ8Threads) p.svmax[i] = 0;
-  }
   const uint32_t total = (uint32_t)off[p.B] * (uint32_t)p.H;
   int held = -1;                             // the (sequence, KV head) whose query is held
   uint32_t qf[NT][D / 64][4];
@@ -561,6 +549,38 @@ __device__ __forceinline__ void q8_pv_run(const Q8Params &p, Q8Shared<D, NT> &sm
   }
 }
 
+// The references sm.m from every thread's share m of the maximum of head tid mod 4 NT,
+// and with a prefix from its splits' maxima too; those go to mfin.  All threads.
+template <int D, int NT>
+__device__ __forceinline__ void q8_final_max(const Q8Params &p, Q8Shared<D, NT> &sm, float *s_red, int b,
+                                             int h, float m) {
+  constexpr int GP = 4 * NT;
+  const int tid = threadIdx.x, i = tid % GP;
+  if (p.splits > 0 && i < p.G) {
+    const float *src = p.pmax + (size_t)h * p.rows + b * p.G + i;
+#pragma unroll 4
+    for (int t = tid / GP; t < p.splits; t += kQ8Threads / GP) m = fmaxf(m, src[(size_t)t * p.H * p.rows]);
+  }
+  s_red[tid] = m;
+  __syncthreads();
+  if (tid < GP) {
+    for (int t = tid + GP; t < kQ8Threads; t += GP) m = fmaxf(m, s_red[t]);
+    sm.m[tid] = q8_reference(m, tid >= p.G);
+    if (p.splits > 0 && tid < p.G) p.mfin[(size_t)b * p.Hq + h * p.G + tid] = m;
+  }
+  __syncthreads();
+}
+
+// The largest value scale of the prefix for each KV head, over its splits.
+__device__ __forceinline__ void q8_final_scale(const Q8Params &p) {
+  for (int h = threadIdx.x; h < p.H; h += kQ8Threads) {
+    float m = 0.f;
+#pragma unroll 4
+    for (int t = 0; t < p.splits; ++t) m = fmaxf(m, p.psv[(size_t)t * p.H + h]);
+    p.svfin[h] = m;
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8Params p) {
   constexpr int GP = 4 * NT;
@@ -574,6 +594,14 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
   const int c = q8_plan(p, off);
   const uint32_t total = (uint32_t)off[p.B] * (uint32_t)p.H;
   pdl_wait();                                // the logits and maxima of q8_logits
+  if (p.splits > 0) {
+    if (blockIdx.x == 0) q8_final_scale(p);
+    // sequences without own keys have no item: their maxima are the prefix's
+    for (uint32_t i = blockIdx.x; i < (uint32_t)p.B * p.H; i += gridDim.x) {
+      const int b = i / (uint32_t)p.H, h = i - (uint32_t)b * p.H;
+      if (off[b] == off[b + 1]) q8_final_max<D, NT>(p, sm, s_red, b, h, -INFINITY);
+    }
+  }
   for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
     const int u = (int)(item / (uint32_t)p.H), h = (int)(item - (uint32_t)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
@@ -585,18 +613,9 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
       const int i = tid % GP;
       float m = -INFINITY;
       for (int t = off[b] + tid / GP; t < off[b + 1]; t += kQ8Threads / GP)
-        m = fmaxf(m, p.cmax[((long long)t * p.H + h) * GP + i]);
-      s_red[tid] = m;
+        m = fmaxf(m, p.cmax[((size_t)t * p.H + h) * GP + i]);
+      q8_final_max<D, NT>(p, sm, s_red, b, h, m);
     }
-    __syncthreads();
-    if (tid < GP) {
-      float m = s_red[tid];
-      for (int t = tid + GP; t < kQ8Threads; t += GP) m = fmaxf(m, s_red[t]);
-      if (p.splits > 0 && tid < p.G)
-        m = fmaxf(m, from_order_bits(p.mrow[(size_t)b * p.Hq + h * p.G + tid]));
-      sm.m[tid] = q8_reference(m, tid >= p.G);
-    }
-    __syncthreads();
     const size_t first = (size_t)(b * p.H + h) * p.ctxp + 64 * p0;   // the run's first key
     const int n = q8_kept_pages<D, NT>(p, sm, np, p.smax + first / 16 * GP);
     float *dst = p.pacc + (size_t)item * p.G * D;
@@ -608,8 +627,10 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
 
 // Short contexts (at most kQ8MaxPages pages of table): a CTA takes all keys of one
 // sequence and KV head, keeps their logits in shared memory and writes the
-// output: one launch and no partial sums.
-template <int D, int NT>
+// output: one launch and no partial sums.  Prefix: the own keys behind a shared
+// prefix, a partial sum for q8_merge; the logits are formed beside the prefix's
+// maximum pass.
+template <int D, int NT, bool Prefix>
 __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const Q8Params p) {
   constexpr int GP = 4 * NT;
   extern __shared__ __align__(16) uint8_t q8_dsm[];
@@ -618,14 +639,16 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
   float *lg = reinterpret_cast<float *>(q8_dsm + sizeof(uint16_t) * pages * 8 * NT * kQ8WRow);
   float *lm = lg + 64 * pages * GP;
   __shared__ Q8Shared<D, NT> sm;
+  __shared__ float s_red[kQ8Threads];
   const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
   const int len = q8_len(p, b), np = (len + 63) >> 6;
+  if constexpr (Prefix) pdl_launch_dependents();
   const size_t at = ((size_t)b * p.Hq + h * p.G) * D;
   auto store = [&](int head, int d, float v) {
     if (p.out_bf16) static_cast<uint16_t *>(p.out)[at + head * D + d] = f32_to_bf16_rn_bits(v);
     else static_cast<float *>(p.out)[at + head * D + d] = v;
   };
-  if (np == 0) {                             // no key: zeros
+  if (!Prefix && np == 0) {                  // no key: zeros
     for (int i = tid; i < p.G * D; i += kQ8Threads) store(0, i, 0.f);
     return;
   }
@@ -636,13 +659,26 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
   q8_logits_run<D, NT>(p, sm, b, h, np, len, true, qf, step,
                        [&](int key, int head, float v) { lg[key * GP + head] = v; },
                        [&](int page, int strip, int head, float v) { lm[(4 * page + strip) * GP + head] = v; });
-  if (tid < GP) sm.m[tid] = q8_reference(q8_warps_max(sm), tid >= p.G);
-  __syncthreads();
+  if constexpr (Prefix) {
+    pdl_wait();                              // the prefix's maxima
+    if (h == 0 && b == 0) q8_final_scale(p);
+    q8_final_max<D, NT>(p, sm, s_red, b, h, tid < GP ? q8_warps_max(sm) : -INFINITY);
+  } else {
+    if (tid < GP) sm.m[tid] = q8_reference(q8_warps_max(sm), tid >= p.G);
+    __syncthreads();
+  }
   const int n = q8_kept_pages<D, NT>(p, sm, np, lm);
-  q8_pv_run<D, NT>(p, sm, wt, h, n, lg, [&](int head, int d, float v) {
-    const float sum = q8_warps_sum(sm, head);
-    store(head, d, sum == 0.f ? 0.f : v / sum);
-  });
+  if constexpr (Prefix) {
+    const size_t item = (size_t)b * p.H + h;
+    float *dst = p.pacc + item * p.G * D;
+    q8_pv_run<D, NT>(p, sm, wt, h, n, lg, [&](int head, int d, float v) { dst[head * D + d] = v; });
+    if (tid < GP) p.psum[item * GP + tid] = q8_warps_sum(sm, tid);
+  } else {
+    q8_pv_run<D, NT>(p, sm, wt, h, n, lg, [&](int head, int d, float v) {
+      const float sum = q8_warps_sum(sm, head);
+      store(head, d, sum == 0.f ? 0.f : v / sum);
+    });
+  }
 }
 
 // out of one query head: the partials of the sequence's items, then those of the
@@ -659,7 +695,7 @@ __global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP)
   const int hq = blockIdx.x, b = blockIdx.y, h = hq / p.G, i = hq - h * p.G;
   const int v = NV * blockIdx.z + threadIdx.x % NV, j = threadIdx.x / NV;
   pdl_wait();
-  const int t0 = p.off[b], own = p.off[b + 1] - t0, nt = own + p.splits;
+  const int t0 = p.single ? b : p.off[b], own = p.single ? 1 : p.off[b + 1] - t0, nt = own + p.splits;
   const int a = (int)((long long)nt * j / J), z = (int)((long long)nt * (j + 1) / J);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
@@ -730,12 +766,13 @@ size_t q8_pv_smem(int NT, int B) {
 }
 
 // One CTA per sequence and KV head where its pages fit a CTA's shared memory and
-// either the context is so short that splitting it gains nothing (four pages) or the
-// CTAs fill the SMs anyway.  Measured (16/2 heads of 128, one launch against three):
-// see the launch rule's figures at launch_q8_attention.
+// splitting them gains nothing: contexts of four pages at most (16/2 heads of 128, 17
+// keys: 4.9 us in one launch, 11.7 us in three), CTAs that fill the SMs anyway, or own
+// keys behind a prefix, whose maximum pass takes longer (24 sequences of up to 300 keys
+// behind 5001: 25 us in four launches, 31 us in five).
 bool q8_is_short(const Q8Shape &s) {
   const int pages = (s.ctx + 63) / 64;
-  return s.prefix == 0 && pages <= kQ8MaxPages && (pages <= 4 || s.B * s.Hkv >= 2 * kQ8Sms);
+  return pages <= kQ8MaxPages && (pages <= 4 || s.prefix > 0 || s.B * s.Hkv >= 2 * kQ8Sms);
 }
 size_t q8_short_smem(int NT, int pages) {
   return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + (64 + 4) * 4 * NT * sizeof(float));
@@ -743,8 +780,11 @@ size_t q8_short_smem(int NT, int pages) {
 
 template <int D, int NT>
 cudaError_t q8_run_short(const Q8Params &p, cudaStream_t st, Launcher &L) {
-  return L.launch("q8_short", q8_short_kernel<D, NT>, dim3((unsigned)p.H, (unsigned)p.B),
-                  dim3(kQ8Threads), q8_short_smem(NT, p.ctxp / 64), st, false, p);
+  const dim3 grid((unsigned)p.H, (unsigned)p.B), block(kQ8Threads);
+  const size_t smem = q8_short_smem(NT, p.ctxp / 64);
+  if (p.splits > 0)
+    return L.launch("q8_short", q8_short_kernel<D, NT, true>, grid, block, smem, st, true, p);
+  return L.launch("q8_short", q8_short_kernel<D, NT, false>, grid, block, smem, st, false, p);
 }
 
 template <int D>
@@ -782,15 +822,24 @@ cudaError_t prepare_q8_kernels() {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)q8_short_smem(NT, kQ8MaxPages));
   };
-  set_short((const void *)q8_short_kernel<64, 1>, 1);
-  set_short((const void *)q8_short_kernel<64, 2>, 2);
-  set_short((const void *)q8_short_kernel<64, 4>, 4);
-  set_short((const void *)q8_short_kernel<128, 1>, 1);
-  set_short((const void *)q8_short_kernel<128, 2>, 2);
-  set_short((const void *)q8_short_kernel<128, 4>, 4);
-  set_short((const void *)q8_short_kernel<256, 1>, 1);
-  set_short((const void *)q8_short_kernel<256, 2>, 2);
-  set_short((const void *)q8_short_kernel<256, 4>, 4);
+  set_short((const void *)q8_short_kernel<64, 1, false>, 1);
+  set_short((const void *)q8_short_kernel<64, 1, true>, 1);
+  set_short((const void *)q8_short_kernel<64, 2, false>, 2);
+  set_short((const void *)q8_short_kernel<64, 2, true>, 2);
+  set_short((const void *)q8_short_kernel<64, 4, false>, 4);
+  set_short((const void *)q8_short_kernel<64, 4, true>, 4);
+  set_short((const void *)q8_short_kernel<128, 1, false>, 1);
+  set_short((const void *)q8_short_kernel<128, 1, true>, 1);
+  set_short((const void *)q8_short_kernel<128, 2, false>, 2);
+  set_short((const void *)q8_short_kernel<128, 2, true>, 2);
+  set_short((const void *)q8_short_kernel<128, 4, false>, 4);
+  set_short((const void *)q8_short_kernel<128, 4, true>, 4);
+  set_short((const void *)q8_short_kernel<256, 1, false>, 1);
+  set_short((const void *)q8_short_kernel<256, 1, true>, 1);
+  set_short((const void *)q8_short_kernel<256, 2, false>, 2);
+  set_short((const void *)q8_short_kernel<256, 2, true>, 2);
+  set_short((const void *)q8_short_kernel<256, 4, false>, 4);
+  set_short((const void *)q8_short_kernel<256, 4, true>, 4);
   set((const void *)q8_pv_kernel<64, 1>, 1);
   set((const void *)q8_pv_kernel<64, 2>, 2);
   set((const void *)q8_pv_kernel<64, 4>, 4);

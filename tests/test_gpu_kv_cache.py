@@ -361,6 +361,21 @@ def test_prefix_longer_with_uneven_value_scales(dv):
     check(out, P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix), PREFIX)
 
 
+@pytest.mark.parametrize("lens,prefix", [([1500, 0, 7], 300), ([5000], 64), ([0, 0], 700), ([1025] * 9, 129)])
+def test_prefix_before_long_own_contexts(dv, lens, prefix):
+    """Own contexts that are split over CTAs (and tables that allow it without using it)."""
+    B = len(lens)
+    q = P.queries(B, 16, 128, seed=sum(lens) + B)
+    for bind in (None, 13.0):
+        pool, table, ptable = P.filled(B, 4, 128, lens, seed=prefix, prefix=prefix, bind=bind and (q, bind))
+        wide = torch.cat([table, torch.full((B, 17), -7, dtype=torch.int32)], 1)
+        c = to_gpu(dv, pool, wide)
+        out = dv.dvssq_bss_attention_prefix(q.cuda(), c, i32(lens), ptable.cuda(), prefix)
+        check(out, P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix), PREFIX)
+        again = dv.dvssq_bss_attention_prefix(q.cuda(), c, i32(lens), ptable.cuda(), prefix)
+        assert torch.equal(out, again)
+
+
 def test_prefix_equals_the_same_keys_in_the_own_table(dv):
     """A page-aligned prefix gives what the decode form gives over the joined page lists."""
     lens, prefix = [40, 7], 256
