@@ -229,8 +229,8 @@ struct PfxSmem {
   static constexpr int nv = step + 128 * 4;              // int [4][2]: live keys, NaN value scales
   static constexpr int svm = nv + 32;                    // uint32 [12]: largest value scales of the converting warps
   static constexpr int bar = svm + 48;
-  static constexpr int bytes = bar + (2 * R + 15) * 8 + 16;
-  static_assert(128 * kQRow <= R * kSlot && 8 * 32 * 36 * 4 <= R * kSlot, "staging fits the ring");
+  static constexpr int bytes = bar + (2 * R + 16) * 8 + 16;
+  static_assert(128 * kQRow <= (R - kPfxConv) * kSlot && 8 * 32 * 36 * 4 <= R * kSlot, "staging fits the ring");
   static_assert(bytes <= 232448, "shared memory of one CTA");
   // tensor memory columns: O, then Q, then the S buffers (64 columns each)
   static constexpr int NS = PV ? 2 : 4;
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   extern __shared__ __align__(1024) uint8_t pfx_sm[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(pfx_sm + L::bar);
   uint64_t *full = bar, *empty = bar + R, *s_full = bar + 2 * R, *s_empty = s_full + 4,
-           *sc_full = s_empty + 4, *w_full = sc_full + 4, *o_full = w_full + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 1);
+           *sc_full = s_empty + 4, *w_full = sc_full + 4, *o_full = w_full + 2, *q_full = o_full + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 1);
   float (*s_a)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sa);
   float (*s_v)[64] = reinterpret_cast<float (*)[64]>(pfx_sm + L::sv);
   float *s_step = reinterpret_cast<float *>(pfx_sm + L::step);
@@ -278,48 +278,12 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     mbar_init(&w_full[0], 8);
     mbar_init(&w_full[1], 8);
     mbar_init(o_full, 1);
+    mbar_init(q_full, 8);
     fence_mbarrier_init();
   }
   if (warp == kPfxMma) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
-  }
-  // Q: a warp per row, all its rows in flight; row r of the tile is query head
-  // h G + r % G of sequence r / G.  Staged as FP16 rows, then into tensor memory.
-  {
-    constexpr int NWARP = kPfxThreads / 32, NR = (128 + NWARP - 1) / NWARP;
-    KvRaw<VPL> raw[NR];
-#pragma unroll
-    for (int u = 0; u < NR; ++u) {
-      const int r = warp + NWARP * u, rr = rt * 128 + r;
-#pragma unroll
-      for (int i = 0; i < VPL / 2; ++i) raw[u].w[i] = 0;
-      if (r < 128 && rr < p.rows) {
-        const int b = rr / G;
-        raw[u] = kv_load<VPL>(p.q8.q + b * p.q8.q_bs + (long long)(h * G + rr - b * G) * p.q8.q_hs + lane * VPL);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < NR; ++u) {
-      const int r = warp + NWARP * u;
-      if (r >= 128) break;
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < VPL / 2; ++i) m = max(m, max(raw[u].w[i] & 0x7FFFu, (raw[u].w[i] >> 16) & 0x7FFFu));
-      m = __reduce_max_sync(0xffffffffu, m);
-      const bool finite = m < 0x7F80u;
-      // times 2^(14 - e) in two exact steps (14 - e is 140 at most)
-      const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100);
-      const float f0 = __int_as_float((up + 127) << 23), f1 = __int_as_float((14 - e - up + 127) << 23);
-      uint8_t *dst = pfx_sm + r * L::kQRow + 2 * lane * VPL;
-#pragma unroll
-      for (int i = 0; i < VPL / 2; ++i) {
-        const __half2 x = __floats2half2_rn(bf16_bits_to_f32(raw[u].w[i] & 0xFFFFu) * f0 * f1,
-                                            bf16_bits_to_f32(raw[u].w[i] >> 16) * f0 * f1);
-        *reinterpret_cast<uint32_t *>(dst + 4 * i) = finite ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
-      }
-      if (lane == 0) s_step[r] = finite ? ldexpf(1.0f, e - 14) : __uint_as_float(0x7FC00000u);
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -329,22 +293,64 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
   const uint32_t tmem = *tmem_slot;
   const long long limit = wait_limit();
   bool ok = true;
-  if (warp < 4) {
-#pragma unroll 1
-    for (int j = 0; j < DB; ++j) {
-      uint32_t w[32];
+  // Q by the warpgroups that do not convert (those fetch their first pages meanwhile): a
+  // warp per row, all its rows in flight; row r of the tile is query head h G + r % G of
+  // sequence r / G.  Staged as FP16 rows in the ring's last slots, then into tensor
+  // memory.
+  if (wg < 2 || wg == 2 + kPfxConv) {
+    constexpr int NW = 12, NR = (128 + NW - 1) / NW;
+    uint8_t *stage = pfx_sm + kPfxConv * L::kSlot;
+    const int w = wg < 2 ? warp : warp - 4 * kPfxConv;
+    KvRaw<VPL> raw[NR];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(pfx_sm + tid * L::kQRow + 128 * j + 16 * i);
-        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+    for (int u = 0; u < NR; ++u) {
+      const int r = w + NW * u, rr = rt * 128 + r;
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) raw[u].w[i] = 0;
+      if (r < 128 && rr < p.rows) {
+        const int b = rr / G;
+        raw[u] = kv_load<VPL>(p.q8.q + b * p.q8.q_bs + (long long)(h * G + rr - b * G) * p.q8.q_hs + lane * VPL);
       }
-      tmem_st32(tmem + ((uint32_t)(32 * warp) << 16) + L::tq + 32 * j, w);
     }
-    tmem_st_wait();
+#pragma unroll
+    for (int u = 0; u < NR; ++u) {
+      const int r = w + NW * u;
+      if (r >= 128) break;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) m = max(m, max(raw[u].w[i] & 0x7FFFu, (raw[u].w[i] >> 16) & 0x7FFFu));
+      m = __reduce_max_sync(0xffffffffu, m);
+      const bool finite = m < 0x7F80u;
+      // times 2^(14 - e) in two exact steps (14 - e is 140 at most)
+      const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100);
+      const float f0 = __int_as_float((up + 127) << 23), f1 = __int_as_float((14 - e - up + 127) << 23);
+      uint8_t *dst = stage + r * L::kQRow + 2 * lane * VPL;
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) {
+        const __half2 x = __floats2half2_rn(bf16_bits_to_f32(raw[u].w[i] & 0xFFFFu) * f0 * f1,
+                                            bf16_bits_to_f32(raw[u].w[i] >> 16) * f0 * f1);
+        *reinterpret_cast<uint32_t *>(dst + 4 * i) = finite ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+      }
+      if (lane == 0) s_step[r] = finite ? ldexpf(1.0f, e - 14) : __uint_as_float(0x7FC00000u);
+    }
+    asm volatile("bar.sync 3, 384;" ::: "memory");
+    if (wg < 2) {
+#pragma unroll 1
+      for (int j = wg; j < DB; j += 2) {             // a warpgroup every other block of 64 dimensions
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(stage + (tid & 127) * L::kQRow + 128 * j + 16 * i);
+          x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        }
+        tmem_st32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::tq + 32 * j, x);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);            // Q is in place and its stage is free
+    }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
 
   if (wg < 2) {
     // ------------------------------- weights -------------------------------
@@ -496,6 +502,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       const bool k = is_k(t);
       bool got = true;
       if (t >= R) got = pfx_wait(&empty[slot], ((t / R) - 1) & 1, limit);
+      else if (t >= kPfxConv) got = pfx_wait(q_full, 0, limit);   // the ring's last slots staged Q
       // the weights of page j - 4 are done with this slot of scales
       if (k && j >= 4) got = got && pfx_wait(&s_empty[sb], ((j >> 2) - 1) & 1, limit);
       if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
@@ -585,7 +592,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         next();
         return true;
       };
-      ok = qk(0);
+      ok = __all_sync(0xffffffffu, pfx_wait(q_full, 0, limit));
+      tc_fence_after();
+      ok = ok && qk(0);
       for (int j = 0; j < n && ok; ++j) {
         if (j + 1 < n) ok = qk(j + 1);
         if constexpr (PV) ok = ok && wv(j);

@@ -573,11 +573,14 @@ __device__ __forceinline__ void q8_final_max(const Q8Params &p, Q8Shared<D, NT> 
 
 // The largest value scale of the prefix for each KV head, over its splits.
 __device__ __forceinline__ void q8_final_scale(const Q8Params &p) {
-  for (int h = threadIdx.x; h < p.H; h += kQ8Threads) {
+  const int lane = threadIdx.x & 31;
+  for (int h = threadIdx.x >> 5; h < p.H; h += kQ8Threads / 32) {
     float m = 0.f;
 #pragma unroll 4
-    for (int t = 0; t < p.splits; ++t) m = fmaxf(m, p.psv[(size_t)t * p.H + h]);
-    p.svfin[h] = m;
+    for (int t = lane; t < p.splits; t += 32) m = fmaxf(m, p.psv[(size_t)t * p.H + h]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) p.svfin[h] = m;
   }
 }
 
