@@ -74,12 +74,12 @@ __device__ __forceinline__ int q8_len(const Q8Params &p, int b) {
 }
 
 // The plan, the same in every CTA: off[b] = items of the sequences before b (per KV
-// head) in shared memory; returns the pages per item c.  N page-heads over r
-// rounds of `target` CTAs, r the fewest whose items stay within kQ8MaxPages; a
-// sequence's last item may be short, so that there are up to N / c + B H items, and
-// c is chosen for those to fit the rounds (a few items over a round would double
-// the time: 20 us instead of 13 for the logits of 32 sequences of up to 8000 keys).
-__device__ __forceinline__ int q8_plan(const Q8Params &p, int *off) {
+// head) in shared memory.  A sequence gets ceil(pages / c) items of even shares.  N
+// page-heads over r rounds of `target` CTAs, r the fewest for at most kQ8MaxPages pages
+// per item; there are up to N / c + B H items, and c is chosen for those to fit the
+// rounds (a few items over a round would double the time: 20 us instead of 13 for the
+// logits of 32 sequences of up to 8000 keys).
+__device__ __forceinline__ void q8_plan(const Q8Params &p, int *off) {
   __shared__ int part[kQ8Threads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.B + kQ8Threads - 1) / kQ8Threads;
@@ -121,7 +121,6 @@ __device__ __forceinline__ int q8_plan(const Q8Params &p, int *off) {
   }
   if (b1 == p.B && b0 < b1) off[p.B] = base;
   __syncthreads();
-  return c;
 }
 
 // Sequence of item u (the last b with off[b] <= u and items of its own)
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
   __shared__ Q8Shared<D, NT> sm;
   const int tid = threadIdx.x;
   pdl_launch_dependents();
-  const int c = q8_plan(p, off);
+  q8_plan(p, off);
   if (blockIdx.x == 0)
     for (int b = tid; b <= p.B; b += kQ8Threads) p.off[b] = off[b];
   const uint32_t total = (uint32_t)off[p.B] * (uint32_t)p.H;
@@ -352,7 +351,9 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
   for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
     const int u = (int)(item / (uint32_t)p.H), h = (int)(item - (uint32_t)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
-    const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
+    const int pages = (len + 63) >> 6, own = off[b + 1] - off[b];
+    const int c = (pages + own - 1) / own;   // even shares of the sequence's pages
+    const int p0 = (u - off[b]) * c, np = min(c, pages - p0);
     __syncthreads();                         // the previous item's shared memory is free
     q8_pages(p, b, p0, np, sm.page);
     __syncthreads();
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
   __shared__ float s_red[kQ8Threads];
   const int tid = threadIdx.x;
   pdl_launch_dependents();
-  const int c = q8_plan(p, off);
+  q8_plan(p, off);
   const uint32_t total = (uint32_t)off[p.B] * (uint32_t)p.H;
   pdl_wait();                                // the logits and maxima of q8_logits
   if (p.splits > 0) {
@@ -608,7 +609,9 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
   for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
     const int u = (int)(item / (uint32_t)p.H), h = (int)(item - (uint32_t)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
-    const int p0 = (u - off[b]) * c, np = min(c, ((len + 63) >> 6) - p0);
+    const int pages = (len + 63) >> 6, own = off[b + 1] - off[b];
+    const int c = (pages + own - 1) / own;   // even shares of the sequence's pages
+    const int p0 = (u - off[b]) * c, np = min(c, pages - p0);
     __syncthreads();                         // the previous item's shared memory is free
     q8_pages(p, b, p0, np, sm.page);
     // the final maximum of each head over the sequence's items
@@ -768,14 +771,14 @@ size_t q8_pv_smem(int NT, int B) {
   return sizeof(uint16_t) * kQ8MaxPages * 8 * NT * kQ8WRow + (size_t)(B + 1) * 4;
 }
 
-// One CTA per sequence and KV head where its pages fit a CTA's shared memory and
-// splitting them gains nothing: contexts of four pages at most (16/2 heads of 128, 17
-// keys: 4.9 us in one launch, 11.7 us in three), CTAs that fill the SMs anyway, or own
-// keys behind a prefix, whose maximum pass takes longer (24 sequences of up to 300 keys
-// behind 5001: 25 us in four launches, 31 us in five).
+// One CTA per sequence and KV head where its pages fit a CTA's shared memory, unless
+// contexts of more than eight pages leave most SMs idle.  Measured, one launch against
+// three (16/4 heads of 256, us): 1 x 64 keys 6.3 / 11.1, 1 x 512 12.3 / 12.3, 16 x 1024
+// 18.5 / 20.5, 80 x 1024 38.9 / 73.3, 200 x 300 28.9 / 49.2.  Own keys behind a prefix
+// always: they run beside its maximum pass.
 bool q8_is_short(const Q8Shape &s) {
   const int pages = (s.ctx + 63) / 64;
-  return pages <= kQ8MaxPages && (pages <= 4 || s.prefix > 0 || s.B * s.Hkv >= 2 * kQ8Sms);
+  return pages <= kQ8MaxPages && (pages <= 8 || s.prefix > 0 || s.B * s.Hkv >= 32);
 }
 size_t q8_short_smem(int NT, int pages) {
   return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + (64 + 4) * 4 * NT * sizeof(float));
