@@ -237,6 +237,31 @@ def test_short_contexts_in_one_launch(dv, Hq, H, d, B, ctx):
     check(dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens)), ref, DECODE)
 
 
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+def test_split_contexts_of_every_head_layout(dv, Hq, H, d):
+    """Contexts past 16 pages go through the split form whatever their head layout."""
+    lens = [1300, 64, 0, 1, 1025]
+    q = P.queries(5, Hq, d, seed=Hq * d)
+    for bind, haze in ((None, 12.0), (14.0, 12.0), (14.0, 0.0)):
+        pool, table, _ = P.filled(5, H, d, lens, seed=H + 7, bind=bind and (q, bind))
+        out = dv.dvssq_bss_attention_q8(q.cuda(), to_gpu(dv, pool, table), i32(lens), haze=haze)
+        check(out, P.attention(q, pool, table, lens, haze=haze), DECODE)
+
+
+@pytest.mark.parametrize("B", [128, 129, 300])
+def test_split_form_over_many_sequences(dv, B):
+    """More sequences than threads plan them, most of them short, a few of them empty or long."""
+    lens = [(53 * i) % 130 for i in range(B)]
+    lens[B // 2] = 1200
+    q = P.queries(B, 8, 64, seed=B)
+    pool, table, _ = P.filled(B, 2, 64, lens, seed=B + 1)
+    c = to_gpu(dv, pool, table)
+    ref = P.attention(q, pool, table, lens)
+    out = dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens))
+    check(out, ref, DECODE)
+    assert (out[[i for i, n in enumerate(lens) if n == 0]] == 0).all()
+
+
 def test_many_short_sequences(dv):
     lens = [(37 * i) % 90 for i in range(600)]
     q = P.queries(600, 4, 64, seed=3)
