@@ -524,13 +524,14 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         if (kt == 0) s_nv[sb][0] = nv;
         if (kt == 0 || kt == 32) reinterpret_cast<uint16_t *>(&s_nv[sb][1])[kt >> 5] = nan;
       }
-      if (t + kPfxConv < jobs) fetch(t + kPfxConv);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&full[slot]);
         if (k) mbar_arrive(&sc_full[sb]);
       }
+      // behind the fence, which would wait for these loads as well
+      if (t + kPfxConv < jobs) fetch(t + kPfxConv);
     }
     if constexpr (!PV) {
       // over the converting warpgroups
