@@ -386,8 +386,9 @@ DVSSQ_API dvssq_status dvssq_kv_read(const dvssq_kv_cache *cache, void *k_out, v
                                      int64_t tokens, const int32_t *start, const int32_t *cu,
                                      void *stream);
 
-/* Bytes of workspace dvssq_bss_attention_q8 needs (host only).  Of `shape`,
- * ctx is an upper bound on the lengths (0 <= lens[b] <= ctx).  Limits: batch
+/* Bytes of workspace dvssq_bss_attention_q8 needs (host only); 0 for short
+ * contexts, whose calls take a NULL workspace.  Of `shape`, ctx is an upper
+ * bound on the lengths (0 <= lens[b] <= ctx).  Limits: batch
  * 1..4096, q_heads a multiple of kv_heads with at most 16 query heads per KV
  * head, kv_heads 1..1024, head_dim 64, 128 or 256, ctx 1..2^24, and
  * batch * kv_heads * ceil(ctx / 64) below 2^31.                             */

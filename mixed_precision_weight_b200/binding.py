@@ -540,11 +540,11 @@ def dvssq_kv_read(cache: KvCache, start: torch.Tensor, cu: torch.Tensor | None =
     sp = _indices(start, "start", cache.batch, index)
     cp = None if cu is None else _indices(cu, "cu", cache.batch + 1, index)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache._k.device)
+        k = cache._v_scale.new_empty(shape)
     else:
         _given(k, "k", shape, torch.bfloat16, index)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache._k.device)
+        v = cache._v_scale.new_empty(shape)
     else:
         _given(v, "v", shape, torch.bfloat16, index)
     s = lib.dvssq_kv_read(cache._ref, k.data_ptr(), v.data_ptr(), shape[0], sp, cp,
@@ -592,22 +592,23 @@ def _attention_q8(q, cache, lens, prefix, prefix_len, tau, haze, ctx, out, y_dty
                                          KV_PAGE * cache.width if ctx is None else int(ctx), tau, haze,
                                          -1 if prefix is None else prefix_len)
     if out is None:
-        out = torch.empty(rows, dtype=dtype, device=cache._k.device)
+        out = torch.empty_like(q, dtype=dtype, memory_format=torch.contiguous_format)
     else:
         _given(out, "out", rows, dtype, index)
-    if workspace is None:
-        workspace, nb = torch.empty(need, dtype=torch.uint8, device=cache._k.device), need
-    else:
+    wp = nb = 0
+    if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on cuda:{index}")
-        nb = workspace.numel() * workspace.element_size()
+        wp, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = cache._k.new_empty(need)
+        wp, nb = workspace.data_ptr(), need
     if prefix is None:
-        s = lib.dvssq_bss_attention_q8(shape, cache._ref, qp, qb, qh, lp, out.data_ptr(), y_dtype,
-                                       workspace.data_ptr(), nb, _current_stream(index))
+        s = lib.dvssq_bss_attention_q8(shape, cache._ref, qp, qb, qh, lp, out.data_ptr(), y_dtype, wp,
+                                       nb, _current_stream(index))
     else:
         s = lib.dvssq_bss_attention_prefix(shape, cache._ref, prefix, prefix_len, qp, qb, qh, lp,
-                                           out.data_ptr(), y_dtype, workspace.data_ptr(), nb,
-                                           _current_stream(index))
+                                           out.data_ptr(), y_dtype, wp, nb, _current_stream(index))
     if s:
         raise DvssqError(s, "dvssq_bss_attention_q8" if prefix is None else "dvssq_bss_attention_prefix")
     return out

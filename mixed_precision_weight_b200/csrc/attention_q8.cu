@@ -814,7 +814,7 @@ cudaError_t q8_run(const Q8Params &p, long long items, cudaStream_t st, Launcher
 }
 }  // namespace
 
-size_t q8_workspace_bytes(const Q8Shape &s) { return q8_is_short(s) ? 256 : q8_layout(s).total; }
+size_t q8_workspace_bytes(const Q8Shape &s) { return q8_is_short(s) ? 0 : q8_layout(s).total; }
 
 cudaError_t prepare_q8_kernels() {
   cudaError_t e = cudaSuccess;

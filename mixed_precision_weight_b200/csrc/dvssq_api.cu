@@ -480,7 +480,9 @@ dvssq_status q8_attention(const dvssq_attn_shape *shape, const dvssq_kv_cache *c
   if (cache->batch != shape->batch || cache->kv_heads != shape->kv_heads ||
       cache->head_dim != shape->head_dim || shape->ctx > 64LL * cache->table_width)
     return DVSSQ_ERR_INVALID_ARG;
-  if (q == nullptr || lens == nullptr || out == nullptr || workspace == nullptr ||
+  // without a prefix both entry points run the decode form
+  const size_t need = prefix_len > 0 ? pfx_workspace_bytes(a.s) : q8_workspace_bytes(a.s);
+  if (q == nullptr || lens == nullptr || out == nullptr || (need > 0 && workspace == nullptr) ||
       (prefix_len > 0 && prefix_table == nullptr))
     return DVSSQ_ERR_INVALID_ARG;
   if (y_dtype != DVSSQ_Y_F32 && y_dtype != DVSSQ_Y_BF16) return DVSSQ_ERR_INVALID_ARG;
@@ -488,8 +490,6 @@ dvssq_status q8_attention(const dvssq_attn_shape *shape, const dvssq_kv_cache *c
   if (!aligned16(q) || !aligned16(out)) return DVSSQ_ERR_MISALIGNED;
   if (!aligned4(lens) || (prefix_len > 0 && !aligned4(prefix_table))) return DVSSQ_ERR_MISALIGNED;
   if (!aligned256(workspace)) return DVSSQ_ERR_MISALIGNED;
-  // without a prefix both entry points run the decode form
-  const size_t need = prefix_len > 0 ? pfx_workspace_bytes(a.s) : q8_workspace_bytes(a.s);
   if (workspace_bytes < need) return DVSSQ_ERR_WORKSPACE;
   if ((s = ensure_device()) != DVSSQ_OK) return s;
   a.q = static_cast<const uint16_t *>(q);

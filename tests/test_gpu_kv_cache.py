@@ -569,7 +569,8 @@ def test_binding_refusals(dv):
     with pytest.raises(dv.DvssqError):
         dv.dvssq_bss_attention_q8(q, c, lens, ctx=10 ** 6)   # longer than the table
     with pytest.raises(dv.DvssqError):
-        dv.dvssq_bss_attention_q8(q, c, lens, workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))
+        dv.dvssq_bss_attention_prefix(q, c, lens, ptable.cuda(), 70,
+                                      workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         dv.dvssq_bss_attention_prefix(q, c, lens, ptable.cuda(), 200)
     with pytest.raises(ValueError):

@@ -44,7 +44,7 @@ BAD_CACHES = [
 
 @pytest.mark.parametrize("kw,status", BAD_CACHES)
 def test_bad_caches_rejected(dv, kw, status):
-    c = cache(dv, **kw)
+    c = cache(dv, **{"table_width": 128, **kw})
     assert append(dv, c) == status
     assert read(dv, c) == status
     if "head_dim" not in kw and "kv_heads" not in kw and "batch" not in kw and "table_width" not in kw:
@@ -68,7 +68,7 @@ def test_append_and_read_argument_checks(dv):
 
 def attend(dv, c, shape=None, q=256, qbs=2048, qhs=128, lens=256, out=256, yd=0, ws=256, wsb=1 << 40,
            prefix=None, plen=0, entry="q8"):
-    sh = dv.AttnShape(3, 16, 4, 128, 128, 1.1, 12.0) if shape is None else shape
+    sh = dv.AttnShape(3, 16, 4, 128, 8192, 1.1, 12.0) if shape is None else shape
     shp = None if sh is False else ctypes.byref(sh)
     cp = None if c is None else ctypes.byref(c)
     if entry == "q8":
@@ -77,9 +77,12 @@ def attend(dv, c, shape=None, q=256, qbs=2048, qhs=128, lens=256, out=256, yd=0,
 
 
 def test_attention_argument_checks(dv):
-    c = cache(dv)
     n = ctypes.c_size_t(0)
-    good = dv.AttnShape(3, 16, 4, 128, 128, 1.1, 12.0)
+    tiny = dv.AttnShape(3, 16, 4, 128, 128, 1.1, 12.0)
+    assert dv.lib.dvssq_bss_attention_q8_workspace_size(ctypes.byref(tiny), ctypes.byref(n)) == 0
+    assert n.value == 0                                                  # one launch, no partial sums
+    c = cache(dv, table_width=128)
+    good = dv.AttnShape(3, 16, 4, 128, 8192, 1.1, 12.0)
     assert dv.lib.dvssq_bss_attention_q8_workspace_size(ctypes.byref(good), ctypes.byref(n)) == 0
     need = n.value
     assert need > 0
@@ -100,7 +103,7 @@ def test_attention_argument_checks(dv):
                        (A(3, 16, 4, 128, 128, 1.1, math.nan), 1),
                        # not the cache's own shape, or longer than its table
                        (A(2, 16, 4, 128, 128, 1.1, 12.0), 1), (A(3, 16, 2, 128, 128, 1.1, 12.0), 1),
-                       (A(3, 16, 4, 256, 128, 1.1, 12.0), 1), (A(3, 16, 4, 128, 129, 1.1, 12.0), 1)):
+                       (A(3, 16, 4, 256, 128, 1.1, 12.0), 1), (A(3, 16, 4, 128, 8193, 1.1, 12.0), 1)):
         assert attend(dv, c, sh) == status, tuple(getattr(sh, f) for f, _ in sh._fields_)
     for entry in ("q8", "prefix"):
         call = lambda cc=c, **kw: attend(dv, cc, entry=entry, **kw)  # noqa: E731
