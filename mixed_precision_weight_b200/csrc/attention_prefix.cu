@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     uint8_t *stage = pfx_sm + kPfxConv * L::kSlot;
     const int w = wg < 2 ? warp : warp - 4 * kPfxConv;
     KvRaw<VPL> raw[NR];
+    uint32_t m[NR];
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
       const int r = w + NW * u, rr = rt * 128 + r;
@@ -312,26 +313,30 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         raw[u] = kv_load<VPL>(p.q8.q + b * p.q8.q_bs + (long long)(h * G + rr - b * G) * p.q8.q_hs + lane * VPL);
       }
     }
+    // (no branch between the rows, so that their reductions overlap)
+#pragma unroll
+    for (int u = 0; u < NR; ++u) {
+      m[u] = 0;
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) m[u] = max(m[u], max(raw[u].w[i] & 0x7FFFu, (raw[u].w[i] >> 16) & 0x7FFFu));
+      m[u] = __reduce_max_sync(0xffffffffu, m[u]);
+    }
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
       const int r = w + NW * u;
-      if (r >= 128) break;
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < VPL / 2; ++i) m = max(m, max(raw[u].w[i] & 0x7FFFu, (raw[u].w[i] >> 16) & 0x7FFFu));
-      m = __reduce_max_sync(0xffffffffu, m);
-      const bool finite = m < 0x7F80u;
-      // times 2^(14 - e) in two exact steps (14 - e is 140 at most)
-      const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100);
-      const float f0 = __int_as_float((up + 127) << 23), f1 = __int_as_float((14 - e - up + 127) << 23);
+      const bool finite = m[u] < 0x7F80u, in = r < 128;
+      // times 2^(14 - e) in two exact steps (14 - e is 140 at most); the step undoes it
+      const int e = max((int)(m[u] >> 7) - 127, -126), up = min(14 - e, 100), rest = 14 - e - up;
+      const float f0 = __int_as_float((127 + up) << 23), f1 = __int_as_float((127 + rest) << 23);
+      const float step = __int_as_float((127 - up) << 23) * __int_as_float((127 - rest) << 23);
       uint8_t *dst = stage + r * L::kQRow + 2 * lane * VPL;
 #pragma unroll
       for (int i = 0; i < VPL / 2; ++i) {
         const __half2 x = __floats2half2_rn(bf16_bits_to_f32(raw[u].w[i] & 0xFFFFu) * f0 * f1,
                                             bf16_bits_to_f32(raw[u].w[i] >> 16) * f0 * f1);
-        *reinterpret_cast<uint32_t *>(dst + 4 * i) = finite ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+        if (in) *reinterpret_cast<uint32_t *>(dst + 4 * i) = finite ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
       }
-      if (lane == 0) s_step[r] = finite ? ldexpf(1.0f, e - 14) : __uint_as_float(0x7FC00000u);
+      if (in && lane == 0) s_step[r] = finite ? step : __uint_as_float(0x7FC00000u);
     }
     asm volatile("bar.sync 3, 384;" ::: "memory");
     if (wg < 2) {

@@ -177,8 +177,8 @@ __device__ __forceinline__ void q8_limbs(const uint16_t *q, int8_t *hi, int8_t *
   m = __reduce_max_sync(0xffffffffu, m);
   const bool finite = m < 0x7F80u;
   // times 2^(14 - e) in two exact steps (14 - e is 140 at most)
-  const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100);
-  const float f0 = __int_as_float((up + 127) << 23), f1 = __int_as_float((14 - e - up + 127) << 23);
+  const int e = max((int)(m >> 7) - 127, -126), up = min(14 - e, 100), rest = 14 - e - up;
+  const float f0 = __int_as_float((127 + up) << 23), f1 = __int_as_float((127 + rest) << 23);
   uint32_t ph[(VPL + 3) / 4], pl[(VPL + 3) / 4];
 #pragma unroll
   for (int i = 0; i < (VPL + 3) / 4; ++i) ph[i] = pl[i] = 0;
@@ -193,7 +193,9 @@ __device__ __forceinline__ void q8_limbs(const uint16_t *q, int8_t *hi, int8_t *
   }
   kv_store_codes<VPL>(hi + lane * VPL, ph);
   kv_store_codes<VPL>(lo + lane * VPL, pl);
-  if (lane == 0) *step = finite ? ldexpf(1.0f, e - 14) : __uint_as_float(0x7FC00000u);
+  if (lane == 0)
+    *step = finite ? __int_as_float((127 - up) << 23) * __int_as_float((127 - rest) << 23)
+                   : __uint_as_float(0x7FC00000u);
 }
 
 // What the two contractions of a run of pages work on, one CTA of four warps.
