@@ -589,7 +589,8 @@ def _attention_q8(q, cache, lens, prefix, prefix_len, tau, haze, ctx, out, y_dty
         raise ValueError("y_dtype must be Y_F32 or Y_BF16")
     dtype = torch.float32 if y_dtype == Y_F32 else torch.bfloat16
     _, shape, need = _attention_q8_shape(B, rows[1], cache.kv_heads, d,
-                                         KV_PAGE * cache.width if ctx is None else int(ctx), tau, haze,
+                                         KV_PAGE * cache.width if ctx is None else int(ctx),
+                                         float(tau), float(haze),
                                          -1 if prefix is None else prefix_len)
     if out is None:
         out = torch.empty_like(q, dtype=dtype, memory_format=torch.contiguous_format)

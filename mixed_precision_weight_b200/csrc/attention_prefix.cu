@@ -26,7 +26,8 @@
 // has 8 significant bits; values 2^29 below the row's largest vanish), so S is
 // FP32-grade.  A weight is rounded once to FP16 (2^-12 relative), scaled by
 // 2^(14 - e) with 2^e at or above the head's largest vs: the rounding holds
-// down to e^-19 of the largest weight, and what underflows is below 2^-38 of it.
+// down to e^-19 of the largest weight, and what underflows is below 2^-38 of it
+// (value scales of 2^-86 to 2^88; outside the weights lose bits towards either end).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       if (sv > 0.f) {
         int e;
         frexpf(sv, &e);                              // vs < 2^e
-        shift = 14 - e;
+        shift = min(14 - e, 100);                    // (the sum of a long prefix stays finite)
       }
       if (m > -INFINITY) {
         x0 = (float)shift - m;                       // exponent of a weight: S ks r2 + x0
@@ -605,7 +606,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         if (j + 1 < n) ok = qk(j + 1);
         if constexpr (PV) ok = ok && wv(j);
       }
-      if constexpr (PV) tc_commit_lead(lead, o_full);
+      if (PV || !ok) tc_commit_lead(lead, o_full);
+      if (!ok) pfx_wait(o_full, 0, limit);           // nothing is in flight when the memory goes
     }
   }
   // what follows waits for this grid only: it ends after the one before it

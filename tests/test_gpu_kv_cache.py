@@ -386,6 +386,34 @@ def test_prefix_longer_with_uneven_value_scales(dv):
     check(out, P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix), PREFIX)
 
 
+def test_prefix_with_tiny_value_scales(dv):
+    """Value scales near 2^-110: the power of two that lifts the weights ends at 2^100, so that
+    their sum stays finite.  The largest weight is then about 2^-11, in FP16 steps of at
+    least 2^-24: sqrt(300) 2^-25 / sqrt(3) over 2^-11 is 6e-4, beside the rounding's 1.4e-4;
+    bound 2e-3."""
+    lens, prefix = [3, 0], 300
+    q = P.queries(2, 16, 128, seed=25)
+    pool, table, ptable = P.filled(2, 4, 128, lens, seed=26, prefix=prefix)
+    pool["vs"] = (pool["vs"].float() * 2.0 ** -105).to(torch.bfloat16)
+    c = to_gpu(dv, pool, table)
+    out = dv.dvssq_bss_attention_prefix(q.cuda(), c, i32(lens), ptable.cuda(), prefix).cpu()
+    ref = P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix)
+    check(out.double() * 2.0 ** 105, ref * 2.0 ** 105, 2e-3)
+
+
+def test_scalars_as_tensors_and_the_default_stream(dv):
+    """tau held in a tensor that changes between calls is read anew; stream 0 is the default stream."""
+    lens = [70]
+    q = P.queries(1, 8, 64, seed=27).cuda()
+    pool, table, _ = P.filled(1, 2, 64, lens, seed=28)
+    c, lg, tau = to_gpu(dv, pool, table), i32(lens), torch.tensor(1.0)
+    a = dv.dvssq_bss_attention_q8(q, c, lg, tau=tau)
+    assert torch.equal(a, dv.dvssq_bss_attention_q8(q, c, lg, tau=1.0))
+    tau.fill_(2.0)
+    b = dv.dvssq_bss_attention_q8(q, c, lg, tau=tau, stream=torch.cuda.default_stream())
+    assert torch.equal(b, dv.dvssq_bss_attention_q8(q, c, lg, tau=2.0, stream=0)) and not torch.equal(a, b)
+
+
 @pytest.mark.parametrize("lens,prefix", [([1500, 0, 7], 300), ([5000], 64), ([0, 0], 700), ([1025] * 9, 129)])
 def test_prefix_before_long_own_contexts(dv, lens, prefix):
     """Own contexts that are split over CTAs (and tables that allow it without using it)."""
