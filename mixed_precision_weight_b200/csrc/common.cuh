@@ -22,7 +22,6 @@ enum DeviceError : uint32_t {
   kErrWaitTmem = 1u << 1,       // a TMEM accumulator wait ran out
   kErrBadShape = 1u << 2,       // a kernel saw a shape it does not support
   kErrWaitGrid = 1u << 3,       // a grid-wide barrier wait ran out
-  kErrBadIndex = 1u << 4,       // a KV-cache index (page, position, length, row) out of range
 };
 
 // Device error word of the library (one translation unit: see libdvssq.cu).

@@ -227,6 +227,8 @@ size_t bss_workspace_bytes(int B, int Hq, int L, int D);
 cudaError_t launch_bss_attention(const BssArgs &a, cudaStream_t st, Launcher &L);
 
 // ------------------------------------------------------------ 8-bit KV cache -
+// Bit of the device error word: an index (page, position, length, row) out of range.
+constexpr uint32_t kErrBadIndex = 1u << 4;
 // The pool of pages and the sequences' page table (device pointers).
 struct KvPool {
   int8_t *k, *v;
