@@ -404,7 +404,13 @@ DVSSQ_API dvssq_status dvssq_bss_attention_q8_workspace_size(const dvssq_attn_sh
  *   lens    int32 [batch] (device); a sequence of length 0 gets zeros
  *   out     [batch][q_heads][head_dim] (device), fp32 or bf16 by y_dtype
  *           (DVSSQ_Y_*; bf16 rounds the fp32 result to nearest even)
- * Logits, maxima, weights and sums are FP32.  Results are deterministic.
+ * The query enters as 16-bit integers of a power-of-two step per head, exact
+ * for values down to 2^-8 of the head's largest magnitude (smaller ones are
+ * off by at most 2^-15 of it); q . k is then exact, logits, maxima,
+ * exponentials and sums are FP32, and a weight times its value scale enters
+ * P V as two BF16 limbs (2^-17 relative).  A key whose weight is zero adds
+ * nothing, whatever its value scale holds; a NaN key row makes its KV head's
+ * outputs NaN.  tau is at most 1e30.  Results are deterministic.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, DEVICE, CUDA. */
 DVSSQ_API dvssq_status dvssq_bss_attention_q8(const dvssq_attn_shape *shape,
                                               const dvssq_kv_cache *cache, const void *q,
@@ -426,8 +432,10 @@ DVSSQ_API dvssq_status dvssq_bss_attention_prefix_workspace_size(const dvssq_att
  * once for the whole batch.
  *   prefix_table  int32 [ceil(prefix_len / 64)] (device; may be NULL when
  *                 prefix_len is 0)
- * A sequence with neither prefix nor own keys gets zeros.  Results are
- * deterministic.
+ * A sequence with neither prefix nor own keys gets zeros.  Arithmetic as in
+ * dvssq_bss_attention_q8, but over the prefix the query is FP16 (exact: scaled
+ * by a power of two per head) and a weight is rounded once to FP16 (2^-12
+ * relative).  Results are deterministic.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, DEVICE, CUDA. */
 DVSSQ_API dvssq_status dvssq_bss_attention_prefix(const dvssq_attn_shape *shape,
                                                   const dvssq_kv_cache *cache,

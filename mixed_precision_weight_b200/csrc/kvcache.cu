@@ -15,8 +15,11 @@
 //
 // One CTA per (run of one sequence's rows inside one page, KV head, K or V):
 // a run's rows are consecutive positions, so the transposed V bytes go out as
-// words.  Work is HBM-bound: 2 d bytes of BF16 and d + 2 bytes of codes and
-// scale per row.
+// words.  Bound by HBM where it is large: 2 d bytes of BF16 and d + 2 bytes of
+// codes and scale per row.  Measured in a graph: 4096 rows of 4 heads of 256, K and V,
+// written and read back in 18.4 us (50 MB, from and to the L2); 28 K such rows read back in
+// 35.0 us (174 MB, floor 26.6 at copy bandwidth); single tokens at launch latency
+// (3 us each).
 #include "common.cuh"
 #include "kernels.h"
 
