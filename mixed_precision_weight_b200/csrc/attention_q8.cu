@@ -14,7 +14,8 @@
 // An item is a run of pages of one sequence and one KV head.  The lengths live
 // on the device, so every CTA derives the same plan from them: pages per item
 // such that the items fill whole rounds of the grid.
-// Short contexts take one launch instead (q8_short: a CTA per sequence and KV head).
+// Contexts up to 64 pages take one launch instead (q8_short: a CTA, or a cluster of
+// them, per sequence and KV head).
 //
 // Measured, 4 sequences of up to 32768 keys, 16/4 heads of 256 (190 MB of keys and
 // values, 29 us at copy bandwidth; the L2 keeps part of them from call to call): 44 us in a
@@ -58,6 +59,7 @@ struct Q8Params {
   const float *po, *pl;
   int splits, rows;
   int single;                    // one item per sequence and KV head, whatever its length
+  int cluster;                   // CTAs per sequence and KV head of the one-launch form
   int B, Hq, H, G, W, n_pages, ctx, ctxp, target;
   float scale2;                  // tau / sqrt(d) log2 e: logits are held in units of log2 e
   float haze2;                   // -haze log2 e; -inf: no truncation
@@ -630,38 +632,42 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
   }
 }
 
-// Short contexts (at most kQ8MaxPages pages of table): a CTA takes all keys of one
-// sequence and KV head, keeps their logits in shared memory and writes the
-// output: one launch and no partial sums.  Prefix: the own keys behind a shared
-// prefix, a partial sum for q8_merge; the logits are formed beside the prefix's
-// maximum pass.
+// One launch: a CTA takes all keys of one sequence and KV head, or a cluster of p.cluster
+// CTAs does, an even share of its pages each (at most kQ8MaxPages); the logits stay
+// in shared memory.  The cluster's CTAs read each other's maxima there, and at the end
+// each a share of the outputs of all partial sums, added in order.
+// Prefix: the own keys behind a shared prefix, a partial sum for q8_merge; the
+// logits are formed beside the prefix's maximum pass.
 template <int D, int NT, bool Prefix>
 __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const Q8Params p) {
   constexpr int GP = 4 * NT;
   extern __shared__ __align__(16) uint8_t q8_dsm[];
-  const int pages = p.ctxp >> 6;
+  const int C = Prefix ? 1 : p.cluster, pages = ((p.ctxp >> 6) + C - 1) / C;
   uint16_t (*wt)[8 * NT][kQ8WRow] = reinterpret_cast<uint16_t (*)[8 * NT][kQ8WRow]>(q8_dsm);
   float *lg = reinterpret_cast<float *>(q8_dsm + sizeof(uint16_t) * pages * 8 * NT * kQ8WRow);
   float *lm = lg + 64 * pages * GP;
+  float *part = lm + 4 * pages * GP;         // [G][D], of a cluster
   __shared__ Q8Shared<D, NT> sm;
   __shared__ float s_red[kQ8Threads];
-  const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
-  const int len = q8_len(p, b), np = (len + 63) >> 6;
+  __shared__ float s_max[GP], s_sum[GP];     // read by the cluster
+  const int tid = threadIdx.x, h = blockIdx.x, rank = blockIdx.y, b = blockIdx.z;
+  const int len = q8_len(p, b), all = (len + 63) >> 6;
+  const int c = (all + C - 1) / C, p0 = min(rank * c, all), np = min(c, all - p0);
   if constexpr (Prefix) pdl_launch_dependents();
   const size_t at = ((size_t)b * p.Hq + h * p.G) * D;
-  auto store = [&](int head, int d, float v) {
-    if (p.out_bf16) static_cast<uint16_t *>(p.out)[at + head * D + d] = f32_to_bf16_rn_bits(v);
-    else static_cast<float *>(p.out)[at + head * D + d] = v;
+  auto store = [&](int i, float v) {
+    if (p.out_bf16) static_cast<uint16_t *>(p.out)[at + i] = f32_to_bf16_rn_bits(v);
+    else static_cast<float *>(p.out)[at + i] = v;
   };
-  if (!Prefix && np == 0) {                  // no key: zeros
-    for (int i = tid; i < p.G * D; i += kQ8Threads) store(0, i, 0.f);
+  if (!Prefix && C == 1 && np == 0) {        // no key: zeros
+    for (int i = tid; i < p.G * D; i += kQ8Threads) store(i, 0.f);
     return;
   }
-  q8_pages(p, b, 0, np, sm.page);
+  q8_pages(p, b, p0, np, sm.page);
   __syncthreads();
   uint32_t qf[NT][D / 64][4];
   float step[NT];
-  q8_logits_run<D, NT>(p, sm, b, h, np, len, true, qf, step,
+  q8_logits_run<D, NT>(p, sm, b, h, np, len - 64 * p0, true, qf, step,
                        [&](int key, int head, float v) { lg[key * GP + head] = v; },
                        [&](int page, int strip, int head, float v) { lm[(4 * page + strip) * GP + head] = v; });
   if constexpr (Prefix) {
@@ -669,7 +675,14 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
     if (h == 0 && b == 0) q8_final_scale(p);
     q8_final_max<D, NT>(p, sm, s_red, b, h, tid < GP ? q8_warps_max(sm) : -INFINITY);
   } else {
-    if (tid < GP) sm.m[tid] = q8_reference(q8_warps_max(sm), tid >= p.G);
+    float m = tid < GP ? q8_warps_max(sm) : -INFINITY;
+    if (C > 1) {
+      if (tid < GP) s_max[tid] = m;
+      cluster_sync();
+      if (tid < GP)
+        for (int r = 0; r < C; ++r) m = fmaxf(m, ld_cluster_f32(cluster_map(smem_u32(&s_max[tid]), r)));
+    }
+    if (tid < GP) sm.m[tid] = q8_reference(m, tid >= p.G);
     __syncthreads();
   }
   const int n = q8_kept_pages<D, NT>(p, sm, np, lm);
@@ -678,11 +691,25 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
     float *dst = p.pacc + item * p.G * D;
     q8_pv_run<D, NT>(p, sm, wt, h, n, lg, [&](int head, int d, float v) { dst[head * D + d] = v; });
     if (tid < GP) p.psum[item * GP + tid] = q8_warps_sum(sm, tid);
-  } else {
+  } else if (C == 1) {
     q8_pv_run<D, NT>(p, sm, wt, h, n, lg, [&](int head, int d, float v) {
       const float sum = q8_warps_sum(sm, head);
-      store(head, d, sum == 0.f ? 0.f : v / sum);
+      store(head * D + d, sum == 0.f ? 0.f : v / sum);
     });
+  } else {
+    q8_pv_run<D, NT>(p, sm, wt, h, n, lg, [&](int head, int d, float v) { part[head * D + d] = v; });
+    if (tid < GP) s_sum[tid] = q8_warps_sum(sm, tid);
+    cluster_sync();
+    for (int i = rank * kQ8Threads + tid; i < p.G * D; i += C * kQ8Threads) {
+      float v = 0.f, sum = 0.f;
+#pragma unroll 4
+      for (int r = 0; r < C; ++r) {
+        sum += ld_cluster_f32(cluster_map(smem_u32(&s_sum[i / D]), r));
+        v += ld_cluster_f32(cluster_map(smem_u32(&part[i]), r));
+      }
+      store(i, sum == 0.f ? 0.f : v / sum);
+    }
+    cluster_sync();                          // the others have read this CTA's share
   }
 }
 
@@ -770,26 +797,46 @@ size_t q8_pv_smem(int NT, int B) {
   return sizeof(uint16_t) * kQ8MaxPages * 8 * NT * kQ8WRow + (size_t)(B + 1) * 4;
 }
 
-// One CTA per sequence and KV head where its pages fit a CTA's shared memory, unless
-// contexts of more than eight pages leave most SMs idle.  Measured, one launch against
-// three (16/4 heads of 256, us): 1 x 64 keys 6.3 / 11.1, 1 x 512 12.3 / 12.3, 16 x 1024
-// 18.5 / 20.5, 80 x 1024 38.9 / 73.3, 200 x 300 28.9 / 49.2.  Own keys behind a prefix
-// always: they run beside its maximum pass.
-bool q8_is_short(const Q8Shape &s) {
-  const int pages = (s.ctx + 63) / 64;
-  return pages <= kQ8MaxPages && (pages <= 8 || s.prefix > 0 || s.B * s.Hkv >= 32);
+// CTAs per sequence and KV head of the one-launch form, 0: three launches.  Up to 16 pages
+// one CTA; a cluster where that leaves SMs idle and there is enough to share.  Up to 64
+// pages the largest cluster that fits the resident CTAs, as long as a CTA gets at most 8
+// pages (16 of 64 dimensions, whose CTA needs less time per page); up to 32 pages 4 CTAs
+// also past that, unless 9 to 16 query heads leave room for one CTA per SM.  Beyond, three
+// launches spread ragged lengths better.  Measured in us (16/4 heads of 256; one launch with
+// 1 / 2 / 4 / 8 CTAs, three launches):
+//   1 x 100 keys 5.5 / 7.5 / 6.5 / 6.5, 9.6        16 x 4096   - / - / 34 / 28, 36
+//   1 x 1024     17.8 / 13.3 / 9.2 / 7.5, 10.2     1 x 8192    - / - / - / 19.8, 17.1
+//   16 x 1024    17.8 / 13.7 / 11.3 / 11.3, 18.1   64 x 1024   32 / 29 / 33 / 41, 36
+//   16 x <= 2048 - / 21.5 / 15.6 / 12.4, 17.5      148 x 1024  51 / 57 / 68 / 86, 64
+// 148 x 4096 of 16/2 heads of 128: - / - / 100 / 100, 87; of 8/8 heads of 64: - / - / 152 / 187, 186.
+// Own keys behind a prefix run beside its maximum pass: one CTA, or the long form.
+int q8_cluster(const Q8Shape &s) {
+  const int pages = (s.ctx + 63) / 64, NT = q8_tiles(s.Hq / s.Hkv);
+  if (s.prefix > 0) return pages <= kQ8MaxPages ? 1 : 0;
+  if (pages > 64) return 0;
+  const int slots = kQ8Sms * q8_occ(NT), rows = s.B * s.Hkv;
+  const bool few = pages <= kQ8MaxPages;
+  int C = 1;
+  if (!few || (pages * s.D > 512 && 4 * rows <= slots))
+    while (C < 8 && 2 * C * rows <= slots && pages > C) C *= 2;
+  if (few) return C;
+  if (s.D == 64) C = std::max(C, pages <= 32 ? 2 : 4);
+  else if (pages <= 32 && NT <= 2) C = std::max(C, 4);
+  return pages <= C * (s.D == 64 ? kQ8MaxPages : 8) ? C : 0;
 }
-size_t q8_short_smem(int NT, int pages) {
-  return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + (64 + 4) * 4 * NT * sizeof(float));
+bool q8_is_short(const Q8Shape &s) { return q8_cluster(s) > 0; }
+size_t q8_short_smem(int NT, int pages, int part) {
+  return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + (64 + 4) * 4 * NT * sizeof(float)) + part * sizeof(float);
 }
 
 template <int D, int NT>
 cudaError_t q8_run_short(const Q8Params &p, cudaStream_t st, Launcher &L) {
-  const dim3 grid((unsigned)p.H, (unsigned)p.B), block(kQ8Threads);
-  const size_t smem = q8_short_smem(NT, p.ctxp / 64);
+  const int C = p.splits > 0 ? 1 : p.cluster;
+  const dim3 grid((unsigned)p.H, (unsigned)C, (unsigned)p.B), block(kQ8Threads);
+  const size_t smem = q8_short_smem(NT, (p.ctxp / 64 + C - 1) / C, C > 1 ? p.G * D : 0);
   if (p.splits > 0)
     return L.launch("q8_short", q8_short_kernel<D, NT, true>, grid, block, smem, st, true, p);
-  return L.launch("q8_short", q8_short_kernel<D, NT, false>, grid, block, smem, st, false, p);
+  return L.launch_ex("q8_short", q8_short_kernel<D, NT, false>, grid, block, smem, st, false, C > 1 ? C : 0, p);
 }
 
 template <int D>
@@ -825,7 +872,7 @@ cudaError_t prepare_q8_kernels() {
   auto set_short = [&](const void *k, int NT) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)q8_short_smem(NT, kQ8MaxPages));
+                               (int)q8_short_smem(NT, kQ8MaxPages, 4 * NT * 256));
   };
   set_short((const void *)q8_short_kernel<64, 1, false>, 1);
   set_short((const void *)q8_short_kernel<64, 1, true>, 1);
@@ -874,6 +921,7 @@ Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
   p.B = a.s.B; p.Hq = a.s.Hq; p.H = a.s.Hkv; p.G = a.s.Hq / a.s.Hkv; p.W = a.pool.W;
   p.n_pages = a.pool.n_pages; p.ctx = a.s.ctx; p.ctxp = (a.s.ctx + 63) / 64 * 64;
   p.target = y.target;
+  p.cluster = q8_cluster(a.s);
   p.scale2 = (float)((double)a.tau / sqrt((double)a.s.D) * 1.4426950408889634);
   p.bits = kKvBits;
   p.haze2 = a.haze > 0.f ? -a.haze * 1.44269504f : -INFINITY;

@@ -262,6 +262,59 @@ def test_split_form_over_many_sequences(dv, B):
     assert (out[[i for i, n in enumerate(lens) if n == 0]] == 0).all()
 
 
+def widened(dv, pool, table, width):
+    """The cache with a table of at least ``width`` pages per sequence, so that the call's bound on the
+    lengths, which picks the kernels, is that of a long context."""
+    more = torch.full((table.shape[0], max(0, width - table.shape[1])), -9, dtype=torch.int32)
+    return to_gpu(dv, pool, torch.cat([table, more], 1).contiguous())
+
+
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+@pytest.mark.parametrize("lens", [[1300, 64, 0, 1, 1025], [513, 0, 512], [2100], [3000, 3, 4096], [70] * 33 + [0, 900]],
+                         ids=lambda x: f"B{len(x)}_{max(x)}")
+def test_every_form_of_every_head_layout(dv, Hq, H, d, lens):
+    """The same sequences with bounds of 1 x, 17, 33 and 65 pages: one CTA, clusters, three launches."""
+    B = len(lens)
+    q = P.queries(B, Hq, d, seed=Hq + d)
+    for bind, haze in ((None, 12.0), (14.0, 0.0)):
+        pool, table, _ = P.filled(B, H, d, lens, seed=H + B, bind=bind and (q, bind))
+        ref = P.attention(q, pool, table, lens, haze=haze)
+        for width in (0, 17, 33, 65):
+            c = widened(dv, pool, table, width)
+            out = dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens), haze=haze)
+            check(out, ref, DECODE)
+            assert torch.equal(out, dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens), haze=haze))
+            b16 = dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens), haze=haze, y_dtype=dv.Y_BF16)
+            assert same_bits(b16, out.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("B", [128, 129, 300])
+@pytest.mark.parametrize("width", [20, 65])
+def test_long_bounds_over_many_sequences(dv, B, width):
+    """As test_split_form_over_many_sequences under a table of more pages than any sequence has."""
+    lens = [(53 * i) % 130 for i in range(B)]
+    lens[B // 2] = 1200
+    q = P.queries(B, 8, 128, seed=B)
+    pool, table, _ = P.filled(B, 2, 128, lens, seed=B + 2)
+    out = dv.dvssq_bss_attention_q8(q.cuda(), widened(dv, pool, table, width), i32(lens))
+    check(out, P.attention(q, pool, table, lens), DECODE)
+    assert (out[[i for i, n in enumerate(lens) if n == 0]] == 0).all()
+
+
+def test_nan_rows_in_every_form(dv):
+    """A sequence of NaN rows is NaN and its neighbours are not, whatever kernels run."""
+    lens = [700, 100, 0]
+    q = P.queries(3, 8, 128, seed=41)
+    pool, table, _ = P.filled(3, 2, 128, lens, seed=42)
+    ref = P.attention(q, pool, table, lens)
+    for p in table[0, :11].tolist():
+        pool["ks"][p] = math.nan
+    for width in (0, 17, 40, 65):
+        out = dv.dvssq_bss_attention_q8(q.cuda(), widened(dv, pool, table, width), i32(lens)).cpu()
+        assert out[0].isnan().all()
+        check(out[1:], ref[1:], DECODE)
+
+
 def test_many_short_sequences(dv):
     lens = [(37 * i) % 90 for i in range(600)]
     q = P.queries(600, 4, 64, seed=3)
