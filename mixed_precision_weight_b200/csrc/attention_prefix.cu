@@ -6,6 +6,7 @@
 // The haze threshold needs each row's final maximum first, so Q K^T runs twice:
 //   pfx_max   S and each split's row maxima, and its largest value scale per KV head
 //   pfx_pv    S again (K comes from L2 now), the weights, and a split's O
+// (A prefix of few page visits is taken by those kernels as well: q8_joins.)
 // Each sequence's own keys go through q8_short, or q8_logits and q8_pv, as without a
 // prefix; those form the maxima over prefix and own keys between the two passes,
 // and q8_merge adds the items' and the splits' partials in order.
@@ -681,7 +682,7 @@ cudaError_t pfx_run(const PfxParams &p, const PfxLayout &y, cudaStream_t st, Lau
 }
 }  // namespace
 
-size_t pfx_workspace_bytes(const Q8Shape &s) { return pfx_layout(s).total; }
+size_t pfx_workspace_bytes(const Q8Shape &s) { return q8_joins(s) ? q8_workspace_bytes(s) : pfx_layout(s).total; }
 
 cudaError_t prepare_prefix_kernels() {
   cudaError_t e = cudaSuccess;
@@ -698,6 +699,7 @@ cudaError_t prepare_prefix_kernels() {
 }
 
 cudaError_t launch_prefix_attention(const Q8Args &a, cudaStream_t st, Launcher &L) {
+  if (q8_joins(a.s)) return launch_q8_attention(a, st, L);
   const PfxLayout y = pfx_layout(a.s);
   char *ws = static_cast<char *>(a.workspace);
   PfxParams p{};

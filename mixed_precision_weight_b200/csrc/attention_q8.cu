@@ -60,6 +60,8 @@ struct Q8Params {
   int splits, rows;
   int single;                    // one item per sequence and KV head, whatever its length
   int cluster;                   // CTAs per sequence and KV head of the one-launch form
+  const int32_t *ptable;         // and a prefix that it takes as the sequences' first keys:
+  int prefix, pp;                // its pages, keys and their number
   int B, Hq, H, G, W, n_pages, ctx, ctxp, target;
   float scale2;                  // tau / sqrt(d) log2 e: logits are held in units of log2 e
   float haze2;                   // -haze log2 e; -inf: no truncation
@@ -85,7 +87,7 @@ __device__ __forceinline__ void q8_plan(const Q8Params &p, int *off) {
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   uint32_t sum = 0;
   for (int b = b0; b < b1; ++b) {
-    const int n = (q8_len(p, b) + 63) >> 6;
+    const int n = p.pp + ((q8_len(p, b) + 63) >> 6);
     off[b] = n;                              // this thread's entries: pages first, then offsets
     sum += n;
   }
@@ -204,7 +206,8 @@ struct Q8Shared {
   float step[4 * NT];
   float m[4 * NT];                           // maxima of the heads
   float warp[kQ8Threads / 32][4 * NT];
-  int page[kQ8MaxPages], list[kQ8MaxPages];
+  int page[kQ8MaxPages], live[kQ8MaxPages];  // ids, and keys that count, of the run's pages
+  int list[kQ8MaxPages];
   uint32_t kept;                             // pages with a key above the threshold
 };
 
@@ -214,15 +217,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
   return r;
 }
 
-// Page ids of a run's pages [p0, p0 + np) of sequence b; -1 outside the pool.
-__device__ __forceinline__ void q8_pages(const Q8Params &p, int b, int p0, int np, int *page) {
+// Ids and live keys of a run's pages [p0, p0 + np) of sequence b, which has len keys of its
+// own; a page outside the pool has none.
+template <int D, int NT>
+__device__ __forceinline__ void q8_pages(const Q8Params &p, Q8Shared<D, NT> &sm, int b, int len, int p0, int np) {
   if (threadIdx.x < np) {
-    int x = p.table[(size_t)b * p.W + p0 + threadIdx.x];
+    const int at = p0 + threadIdx.x, w = at - p.pp;
+    int x = w < 0 ? p.ptable[at] : p.table[(size_t)b * p.W + w];
+    int n = w < 0 ? p.prefix - 64 * at : len - 64 * w;
     if (x < 0 || x >= p.n_pages) {
       set_error(kErrBadIndex);
       x = -1;
+      n = 0;
     }
-    page[threadIdx.x] = x;
+    sm.page[threadIdx.x] = x;
+    sm.live[threadIdx.x] = n;
   }
 }
 
@@ -233,7 +242,7 @@ __device__ __forceinline__ void q8_pages(const Q8Params &p, int b, int p0, int n
 // prepared; `fresh`: the query's limbs and fragments are not those held.
 template <int D, int NT, class Put, class PutMax>
 __device__ __forceinline__ void q8_logits_run(const Q8Params &p, Q8Shared<D, NT> &sm, int b, int h,
-                                              int np, int live, bool fresh, uint32_t (&qf)[NT][D / 64][4],
+                                              int np, bool fresh, uint32_t (&qf)[NT][D / 64][4],
                                               float (&step)[NT], Put put, PutMax put_max) {
   constexpr int DB = D / 64;                 // 64-byte blocks of a K row
   constexpr int DEPTH = 8 / DB;              // pages in flight per warp
@@ -301,10 +310,10 @@ __device__ __forceinline__ void q8_logits_run(const Q8Params &p, Q8Shared<D, NT>
                    word(buf[d][j][0], 2 * s + 1), word(buf[d][j][1], 2 * s + 1), qf[nt][j][2 * s],
                    qf[nt][j][2 * s + 1]);
       const float k0 = bf16_bits_to_f32(sc[d][0]), k1 = bf16_bits_to_f32(sc[d][1]);
-      const bool ok = sm.page[pp] >= 0;
+      const int live = sm.live[pp];
       if (pp + DEPTH < np) issue(pp + DEPTH, buf[d], sc[d]);
       const int at = 64 * pp + key;
-      const bool v0 = ok && at < live, v1 = ok && at + 8 < live;
+      const bool v0 = key < live, v1 = key + 8 < live;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         // 256 hi + lo in exact integers, rounded once to FP32
@@ -352,15 +361,15 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_logits_kernel(const
   for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
     const int u = (int)(item / (uint32_t)p.H), h = (int)(item - (uint32_t)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
-    const int pages = (len + 63) >> 6, own = off[b + 1] - off[b];
+    const int pages = p.pp + ((len + 63) >> 6), own = off[b + 1] - off[b];
     const int c = (pages + own - 1) / own;   // even shares of the sequence's pages
     const int p0 = (u - off[b]) * c, np = min(c, pages - p0);
     __syncthreads();                         // the previous item's shared memory is free
-    q8_pages(p, b, p0, np, sm.page);
+    q8_pages(p, sm, b, len, p0, np);
     __syncthreads();
     float *lg = p.logit + ((size_t)(b * p.H + h) * p.ctxp + 64 * p0) * GP;
     float *lm = p.smax + ((size_t)(b * p.H + h) * (p.ctxp >> 6) + p0) * 4 * GP;
-    q8_logits_run<D, NT>(p, sm, b, h, np, len - 64 * p0, held != b * p.H + h, qf, step,
+    q8_logits_run<D, NT>(p, sm, b, h, np, held != b * p.H + h, qf, step,
                          [&](int key, int head, float v) { lg[key * GP + head] = v; },
                          [&](int page, int strip, int head, float v) { lm[(4 * page + strip) * GP + head] = v; });
     held = b * p.H + h;
@@ -610,11 +619,11 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
   for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
     const int u = (int)(item / (uint32_t)p.H), h = (int)(item - (uint32_t)u * p.H);
     const int b = q8_find(off, p.B, u), len = q8_len(p, b);
-    const int pages = (len + 63) >> 6, own = off[b + 1] - off[b];
+    const int pages = p.pp + ((len + 63) >> 6), own = off[b + 1] - off[b];
     const int c = (pages + own - 1) / own;   // even shares of the sequence's pages
     const int p0 = (u - off[b]) * c, np = min(c, pages - p0);
     __syncthreads();                         // the previous item's shared memory is free
-    q8_pages(p, b, p0, np, sm.page);
+    q8_pages(p, sm, b, len, p0, np);
     // the final maximum of each head over the sequence's items
     {
       const int i = tid % GP;
@@ -636,8 +645,8 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_pv_kernel(const Q8P
 // CTAs does, an even share of its pages each (at most kQ8MaxPages); the logits stay
 // in shared memory.  The cluster's CTAs read each other's maxima there, and at the end
 // each a share of the outputs of all partial sums, added in order.
-// Prefix: the own keys behind a shared prefix, a partial sum for q8_merge; the
-// logits are formed beside the prefix's maximum pass.
+// Prefix: the own keys behind a shared prefix that the prefix kernels take: one CTA, a partial
+// sum for q8_merge; the logits are formed beside the prefix's maximum pass.
 template <int D, int NT, bool Prefix>
 __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const Q8Params p) {
   constexpr int GP = 4 * NT;
@@ -651,7 +660,7 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
   __shared__ float s_red[kQ8Threads];
   __shared__ float s_max[GP], s_sum[GP];     // read by the cluster
   const int tid = threadIdx.x, h = blockIdx.x, rank = blockIdx.y, b = blockIdx.z;
-  const int len = q8_len(p, b), all = (len + 63) >> 6;
+  const int len = q8_len(p, b), all = p.pp + ((len + 63) >> 6);
   const int c = (all + C - 1) / C, p0 = min(rank * c, all), np = min(c, all - p0);
   if constexpr (Prefix) pdl_launch_dependents();
   const size_t at = ((size_t)b * p.Hq + h * p.G) * D;
@@ -663,11 +672,11 @@ __global__ void __launch_bounds__(kQ8Threads, q8_occ(NT)) q8_short_kernel(const 
     for (int i = tid; i < p.G * D; i += kQ8Threads) store(i, 0.f);
     return;
   }
-  q8_pages(p, b, p0, np, sm.page);
+  q8_pages(p, sm, b, len, p0, np);
   __syncthreads();
   uint32_t qf[NT][D / 64][4];
   float step[NT];
-  q8_logits_run<D, NT>(p, sm, b, h, np, len - 64 * p0, true, qf, step,
+  q8_logits_run<D, NT>(p, sm, b, h, np, true, qf, step,
                        [&](int key, int head, float v) { lg[key * GP + head] = v; },
                        [&](int page, int strip, int head, float v) { lm[(4 * page + strip) * GP + head] = v; });
   if constexpr (Prefix) {
@@ -764,6 +773,7 @@ __global__ void __launch_bounds__(256) q8_merge_kernel(const Q8Params p, int GP)
 }
 
 namespace {
+int q8_pages_max(const Q8Shape &s);
 struct Q8Layout {
   size_t logit, smax, cmax, psum, pacc, off, total;
   int target;
@@ -773,7 +783,7 @@ struct Q8Layout {
 Q8Layout q8_layout(const Q8Shape &s) {
   Q8Layout y{};
   const int G = s.Hq / s.Hkv, NT = q8_tiles(G);
-  const long long pages = (s.ctx + 63) / 64;
+  const long long pages = q8_pages_max(s);
   y.target = kQ8Sms * q8_occ(NT);
   const long long N = pages * s.B * s.Hkv, round = (long long)y.target * kQ8MaxPages;
   y.items = std::min(N, y.target * ((N + round - 1) / round) + (long long)s.B * s.Hkv);
@@ -809,12 +819,9 @@ size_t q8_pv_smem(int NT, int B) {
 //   16 x 1024    17.8 / 13.7 / 11.3 / 11.3, 18.1   64 x 1024   32 / 29 / 33 / 41, 36
 //   16 x <= 2048 - / 21.5 / 15.6 / 12.4, 17.5      148 x 1024  51 / 57 / 68 / 86, 64
 // 148 x 4096 of 16/2 heads of 128: - / - / 100 / 100, 87; of 8/8 heads of 64: - / - / 152 / 187, 186.
-// Own keys behind a prefix run beside its maximum pass: one CTA, or the long form.
-int q8_cluster(const Q8Shape &s) {
-  const int pages = (s.ctx + 63) / 64, NT = q8_tiles(s.Hq / s.Hkv);
-  if (s.prefix > 0) return pages <= kQ8MaxPages ? 1 : 0;
+int q8_cluster(const Q8Shape &s, int pages) {
   if (pages > 64) return 0;
-  const int slots = kQ8Sms * q8_occ(NT), rows = s.B * s.Hkv;
+  const int NT = q8_tiles(s.Hq / s.Hkv), slots = kQ8Sms * q8_occ(NT), rows = s.B * s.Hkv;
   const bool few = pages <= kQ8MaxPages;
   int C = 1;
   if (!few || (pages * s.D > 512 && 4 * rows <= slots))
@@ -824,7 +831,29 @@ int q8_cluster(const Q8Shape &s) {
   else if (pages <= 32 && NT <= 2) C = std::max(C, 4);
   return pages <= C * (s.D == 64 ? kQ8MaxPages : 8) ? C : 0;
 }
-bool q8_is_short(const Q8Shape &s) { return q8_cluster(s) > 0; }
+// Whether a prefix is taken as the first keys of each sequence, which reads it once per
+// sequence (from the L2 after the first) but without the prefix kernels' four launches and
+// preparation of Q.  Measured in us, these kernels / the prefix kernels, by page visits
+// (sequences x KV heads x pages of the prefix):
+//   16/4 heads of 256: 4 x 512 keys (128 visits) 7.9 / 18, 16 x 3000 (3008) 19 / 29,
+//   4 x 16000 (4000) 28 / 33, 8 x 9000 (4512) 30 / 29, 48 x 1900 (5760) 34 / 29;
+//   16/2 of 128: 24 x 5001 (3792) 24 / 25, 48 x 3000 (4512) 27 / 26; 8/8 of 64: 24 x 1900
+//   (5760) 15 / 20, 24 x 3000 (9024) 24 / 21; 32/2 of 256: 16 x 5001 (2528) 34 / 36,
+//   48 x 1900 (2880) 38 / 38, 8 x 16000 (4000) 46 / 38.
+bool q8_joins(const Q8Shape &s) {
+  const long long rows = (long long)s.B * s.Hkv, pages = (s.prefix + 63) / 64;
+  return s.prefix > 0 && rows * pages <= (s.Hq / s.Hkv <= 8 ? 4096 : 2400) &&
+         rows * (pages + (s.ctx + 63) / 64) <= INT32_MAX;
+}
+// Pages of a sequence at most, as these kernels take it.
+int q8_pages_max(const Q8Shape &s) {
+  return (s.ctx + 63) / 64 + (q8_joins(s) ? (s.prefix + 63) / 64 : 0);
+}
+// Whether the (own) keys of a sequence take one launch.
+bool q8_is_short(const Q8Shape &s) {
+  if (s.prefix > 0 && !q8_joins(s)) return (s.ctx + 63) / 64 <= kQ8MaxPages;
+  return q8_cluster(s, q8_pages_max(s)) > 0;
+}
 size_t q8_short_smem(int NT, int pages, int part) {
   return (size_t)pages * (sizeof(uint16_t) * 8 * NT * kQ8WRow + (64 + 4) * 4 * NT * sizeof(float)) + part * sizeof(float);
 }
@@ -921,7 +950,6 @@ Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
   p.B = a.s.B; p.Hq = a.s.Hq; p.H = a.s.Hkv; p.G = a.s.Hq / a.s.Hkv; p.W = a.pool.W;
   p.n_pages = a.pool.n_pages; p.ctx = a.s.ctx; p.ctxp = (a.s.ctx + 63) / 64 * 64;
   p.target = y.target;
-  p.cluster = q8_cluster(a.s);
   p.scale2 = (float)((double)a.tau / sqrt((double)a.s.D) * 1.4426950408889634);
   p.bits = kKvBits;
   p.haze2 = a.haze > 0.f ? -a.haze * 1.44269504f : -INFINITY;
@@ -931,8 +959,13 @@ Q8Params q8_params(const Q8Args &a, const Q8Layout &y) {
 
 cudaError_t launch_q8_attention(const Q8Args &a, cudaStream_t st, Launcher &L) {
   const Q8Layout y = q8_layout(a.s);
-  const Q8Params p = q8_params(a, y);
-  const bool once = q8_is_short(a.s);
+  Q8Params p = q8_params(a, y);
+  p.ctxp = 64 * q8_pages_max(a.s);
+  p.cluster = q8_cluster(a.s, p.ctxp / 64);
+  if (a.s.prefix > 0) {
+    p.ptable = a.ptable; p.prefix = a.s.prefix; p.pp = (a.s.prefix + 63) / 64;
+  }
+  const bool once = p.cluster > 0;
   const int NT = q8_tiles(p.G);
 #define Q8_CASE(D_, N_) \
   if (a.s.D == D_ && NT == N_)                            \

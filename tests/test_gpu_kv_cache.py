@@ -467,6 +467,82 @@ def test_scalars_as_tensors_and_the_default_stream(dv):
     assert torch.equal(b, dv.dvssq_bss_attention_q8(q, c, lg, tau=2.0, stream=0)) and not torch.equal(a, b)
 
 
+# Enough visits (sequences x KV heads x pages) that the prefix is read once for all sequences.
+SHARED = [(16, 4, 256, [5, 0, 64] * 6, 4100), (16, 2, 128, [0, 70, 1] * 12, 3800),
+          (6, 2, 128, [3, 70, 1, 0, 65] * 10, 2625), (8, 8, 64, [17] * 40, 897), (20, 4, 64, [1, 2] * 40, 1000),
+          (10, 2, 256, [100, 0] * 20, 3500), (16, 1, 128, [9] * 60, 2700), (32, 2, 256, [30, 0, 2] * 10, 2600),
+          (7, 7, 128, [0, 1] * 300, 64), (7, 7, 64, [0, 3] * 300, 1), (14, 7, 64, [1, 0] * 300, 63),
+          (5, 5, 128, [1, 0] * 250, 129), (9, 1, 64, [4, 0] * 650, 100), (16, 4, 128, [1500, 0, 7] * 6, 3800)]
+
+
+@pytest.mark.parametrize("Hq,H,d,lens,prefix", SHARED)
+def test_prefix_read_once_matches_plain(dv, Hq, H, d, lens, prefix):
+    B = len(lens)
+    assert B * H * -(-prefix // 64) > (4096 if Hq // H <= 8 else 2400)
+    q = P.queries(B, Hq, d, seed=prefix + d)
+    for bind, haze in ((None, 12.0), (15.0, 12.0), (15.0, 0.0)):
+        pool, table, ptable = P.filled(B, H, d, lens, seed=prefix, prefix=prefix, bind=bind and (q, bind))
+        ref = P.attention(q, pool, table, lens, haze=haze, ptable=ptable, prefix=prefix)
+        c = to_gpu(dv, pool, table)
+        args = (q.cuda(), c, i32(lens), ptable.cuda(), prefix)
+        out = dv.dvssq_bss_attention_prefix(*args, haze=haze)
+        check(out, ref, PREFIX)
+        b16 = dv.dvssq_bss_attention_prefix(*args, haze=haze, y_dtype=dv.Y_BF16)
+        assert same_bits(b16, out.to(torch.bfloat16))
+        assert torch.equal(out, dv.dvssq_bss_attention_prefix(*args, haze=haze))
+
+
+def test_prefix_read_once_with_uneven_and_tiny_value_scales(dv):
+    """As the two tests above; tiny scales: sqrt(1000) 2^-25 / sqrt(3) over 2^-11 is 1.1e-3, bound 3e-3."""
+    lens, prefix = [33, 0, 200] * 12, 4100
+    q = P.queries(36, 16, 128, seed=20)
+    pool, table, ptable = P.filled(36, 2, 128, lens, seed=21, prefix=prefix)
+    g = torch.Generator().manual_seed(22)
+    f = torch.exp(torch.empty(pool["vs"].shape).uniform_(-9.0, 0.0, generator=g))
+    pool["vs"] = (pool["vs"].float() * f).to(torch.bfloat16)
+    out = dv.dvssq_bss_attention_prefix(q.cuda(), to_gpu(dv, pool, table), i32(lens), ptable.cuda(), prefix)
+    check(out, P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix), PREFIX)
+    lens, prefix = [3, 0] * 40, 1000
+    q = P.queries(80, 16, 128, seed=25)
+    pool, table, ptable = P.filled(80, 4, 128, lens, seed=26, prefix=prefix)
+    pool["vs"] = (pool["vs"].float() * 2.0 ** -105).to(torch.bfloat16)
+    out = dv.dvssq_bss_attention_prefix(q.cuda(), to_gpu(dv, pool, table), i32(lens), ptable.cuda(), prefix).cpu()
+    check(out.double() * 2.0 ** 105, P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix) * 2.0 ** 105, 3e-3)
+
+
+def test_prefix_read_once_nan_rows_and_bad_pages(dv):
+    lens, prefix = [1, 3, 0] * 100, 1000
+    q = P.queries(300, 4, 64, seed=16)
+    pool, table, ptable = P.filled(300, 2, 64, lens, seed=17, prefix=prefix)
+    pool["ks"].nan_to_num_(0.01)
+    pool["vs"].nan_to_num_(0.01)
+    c = to_gpu(dv, pool, table)
+    bad = ptable.clone()
+    bad[15] = pool["k"].shape[0]                             # the last 40 keys
+    out = dv.dvssq_bss_attention_prefix(q.cuda(), c, i32(lens), bad.cuda(), prefix)
+    assert dv.dvssq_device_error(clear=True) == 16
+    check(out, P.attention(q, pool, table, lens, ptable=ptable, prefix=960), PREFIX)
+    pool["ks"][int(ptable[3]), 1, 5] = math.nan
+    out = dv.dvssq_bss_attention_prefix(q.cuda(), to_gpu(dv, pool, table), i32(lens), ptable.cuda(), prefix).cpu()
+    assert out[:, 2:].isnan().all()
+    pool["ks"][int(ptable[3]), 1, 5] = 0.01
+    check(out[:, :2], P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix)[:, :2], PREFIX)
+    pool["ks"][:] = math.nan
+    assert dv.dvssq_bss_attention_prefix(q.cuda(), to_gpu(dv, pool, table), i32(lens), ptable.cuda(), prefix).isnan().all()
+
+
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+@pytest.mark.parametrize("prefix,lens", [(1000, [70, 0, 300]), (4000, [0, 130, 5]), (6000, [2000]), (65, [1, 0])])
+def test_prefix_as_first_keys(dv, Hq, H, d, prefix, lens):
+    """Prefixes of few visits, in one launch and in three: the arithmetic of the form without a prefix."""
+    B = len(lens)
+    q = P.queries(B, Hq, d, seed=prefix)
+    for bind in (None, 14.0):
+        pool, table, ptable = P.filled(B, H, d, lens, seed=prefix + H, prefix=prefix, bind=bind and (q, bind))
+        out = dv.dvssq_bss_attention_prefix(q.cuda(), to_gpu(dv, pool, table), i32(lens), ptable.cuda(), prefix)
+        check(out, P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix), DECODE)
+
+
 @pytest.mark.parametrize("lens,prefix", [([1500, 0, 7], 300), ([5000], 64), ([0, 0], 700), ([1025] * 9, 129)])
 def test_prefix_before_long_own_contexts(dv, lens, prefix):
     """Own contexts that are split over CTAs (and tables that allow it without using it)."""
@@ -650,7 +726,7 @@ def test_binding_refusals(dv):
     with pytest.raises(dv.DvssqError):
         dv.dvssq_bss_attention_q8(q, c, lens, ctx=10 ** 6)   # longer than the table
     with pytest.raises(dv.DvssqError):
-        dv.dvssq_bss_attention_prefix(q, c, lens, ptable.cuda(), 70,
+        dv.dvssq_bss_attention_prefix(q, widened(dv, pool, table, 65), lens, ptable.cuda(), 70,
                                       workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         dv.dvssq_bss_attention_prefix(q, c, lens, ptable.cuda(), 200)
