@@ -460,9 +460,29 @@ class KvCache:
     def __init__(self, k, v, k_scale, v_scale, table):
         if k.dim() != 4 or table.dim() != 2:
             raise ValueError("k must be [pages][kv_heads][64][d] and table [batch][width]")
-        P, H, _, d = k.shape
+        P, H, n, d = k.shape
         B, W = table.shape
         index = k.get_device()
+        scales = (P, H, KV_PAGE)
+        # (built anew in many a decode step: plain reads here, the message elsewhere)
+        if not (k.dtype is torch.int8 is v.dtype and table.dtype is torch.int32
+                and k_scale.dtype is torch.bfloat16 is v_scale.dtype
+                and n == KV_PAGE and v.shape == (P, H, d, KV_PAGE)
+                and k_scale.shape == scales and v_scale.shape == scales
+                and k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous() and table.is_contiguous()
+                and v.get_device() == k_scale.get_device() == v_scale.get_device() == table.get_device()
+                == index >= 0):
+            self._refuse(k, v, k_scale, v_scale, table)
+        self._k, self._v, self._k_scale, self._v_scale, self._table = k, v, k_scale, v_scale, table
+        self.index, self.batch, self.width, self.kv_heads, self.head_dim = index, B, W, H, d
+        self._c = _KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                            table.data_ptr(), P, H, d, B, W)
+        self._ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def _refuse(k, v, k_scale, v_scale, table):
+        (P, H, _, d), (B, W), index = k.shape, table.shape, k.get_device()
         for t, name, dtype, shape in ((k, "k", torch.int8, (P, H, KV_PAGE, d)),
                                       (v, "v", torch.int8, (P, H, d, KV_PAGE)),
                                       (k_scale, "k_scale", torch.bfloat16, (P, H, KV_PAGE)),
@@ -474,11 +494,6 @@ class KvCache:
                 raise ValueError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
             if t.get_device() != index or index < 0:
                 raise ValueError(f"{name} is on {t.device}: the cache lives on one CUDA device")
-        self._k, self._v, self._k_scale, self._v_scale, self._table = k, v, k_scale, v_scale, table
-        self.index, self.batch, self.width, self.kv_heads, self.head_dim = index, B, W, H, d
-        self._c = _KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                            table.data_ptr(), P, H, d, B, W)
-        self._ref = ctypes.byref(self._c)
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
@@ -544,7 +559,7 @@ def dvssq_kv_read(cache: KvCache, start: torch.Tensor, cu: torch.Tensor | None =
     else:
         _given(k, "k", shape, torch.bfloat16, index)
     if v is None:
-        v = cache._v_scale.new_empty(shape)
+        v = torch.empty_like(k)
     else:
         _given(v, "v", shape, torch.bfloat16, index)
     s = lib.dvssq_kv_read(cache._ref, k.data_ptr(), v.data_ptr(), shape[0], sp, cp,

@@ -17,8 +17,8 @@
 // a run's rows are consecutive positions, so the transposed V bytes go out as
 // words.  Bound by HBM where it is large: 2 d bytes of BF16 and d + 2 bytes of
 // codes and scale per row.  Measured in a graph: 4096 rows of 4 heads of 256, K and V,
-// written and read back in 18.4 us (50 MB, from and to the L2); 28 K such rows read back in
-// 35.0 us (174 MB, floor 26.6 at copy bandwidth); single tokens at launch latency
+// written and read back in 17.1 us (50 MB, from and to the L2); 28 K such rows read back in
+// 33.0 us (174 MB, floor 26.6 at copy bandwidth); single tokens at launch latency
 // (3 us each).
 #include "common.cuh"
 #include "kernels.h"
@@ -299,7 +299,9 @@ __device__ __forceinline__ uint32_t kv_bf16_pair(uint32_t x, const KvBits &k) {
 }
 
 // D threads, four 16-byte pieces of the page each.
-//   K: a piece is 16 dimensions of one row: 32 contiguous bytes out.
+//   K: a piece is 16 dimensions of one row: 32 contiguous bytes out, which two lanes write
+//      whole, one piece each per store (28 K rows: 33 us; as two half sectors 35; the same
+//      trade for V, 16-byte stores for its 8-byte ones, was slower: 36).
 //   V: a warp takes 32 dimensions; a lane 4 of them (one piece each) x 16 tokens, so that
 //      after a transposition of the BF16 results in registers every token's 4
 //      dimensions are 8 contiguous bytes and 8 lanes fill 64.  No shared memory.
@@ -323,6 +325,8 @@ __global__ void __launch_bounds__(D) kv_read_kernel(const KvReadParams p) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int row = (tid + D * x) / CPR;
+      c[x] = make_uint4(0, 0, 0, 0);
+      s[x] = 0;
       if (row >= s0 && row < s1) {
         c[x] = __ldg(reinterpret_cast<const uint4 *>(src) + tid + D * x);
         s[x] = p.ks[ph * 64 + row] * 0x10001u;
@@ -331,7 +335,6 @@ __global__ void __launch_bounds__(D) kv_read_kernel(const KvReadParams p) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int row = (tid + D * x) / CPR, ch = (tid + D * x) % CPR;
-      if (row < s0 || row >= s1) continue;
       const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
       uint32_t o[8];
 #pragma unroll
@@ -340,9 +343,17 @@ __global__ void __launch_bounds__(D) kv_read_kernel(const KvReadParams p) {
         o[2 * i] = __byte_perm(e, f, 0x5410);
         o[2 * i + 1] = __byte_perm(e, f, 0x7632);
       }
-      uint4 *out = reinterpret_cast<uint4 *>(dst + row * ts + 16 * ch);
+      // a pair of lanes holds two pieces of 32 bytes; each store writes one of them whole
+      const bool odd = lane & 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[4 + i], 1);
+        if (odd) o[i] = got; else o[4 + i] = got;
+      }
+      if (row < s0 || row >= s1) continue;
+      uint4 *out = reinterpret_cast<uint4 *>(dst + row * ts + 16 * (ch & ~1)) + odd;
       out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      out[2] = make_uint4(o[4], o[5], o[6], o[7]);
     }
     return;
   }
