@@ -386,8 +386,8 @@ DVSSQ_API dvssq_status dvssq_kv_read(const dvssq_kv_cache *cache, void *k_out, v
                                      int64_t tokens, const int32_t *start, const int32_t *cu,
                                      void *stream);
 
-/* Bytes of workspace dvssq_bss_attention_q8 needs (host only); 0 for short
- * contexts, whose calls take a NULL workspace.  Of `shape`, ctx is an upper
+/* Bytes of workspace dvssq_bss_attention_q8 needs (host only); 0 for contexts
+ * that take one launch, whose calls take a NULL workspace.  Of `shape`, ctx is an upper
  * bound on the lengths (0 <= lens[b] <= ctx).  Limits: batch
  * 1..4096, q_heads a multiple of kv_heads with at most 16 query heads per KV
  * head, kv_heads 1..1024, head_dim 64, 128 or 256, ctx 1..2^24, and
@@ -428,14 +428,16 @@ DVSSQ_API dvssq_status dvssq_bss_attention_prefix_workspace_size(const dvssq_att
 /* dvssq_bss_attention_q8 for a batch whose sequences share a prefix: every
  * sequence attends to the prefix_len keys of the pages prefix_table lists and
  * then to its own lens[b] keys (the cache's table holds its own part only, from
- * its own position 0; the prefix may end inside a page).  The prefix is read
- * once for the whole batch.
+ * its own position 0; the prefix may end inside a page).  A prefix of more
+ * than 4096 page visits (batch x kv_heads x pages; 2400 with more than 8 query
+ * heads per KV head) is read once for the whole batch; a smaller one is read
+ * like each sequence's own keys, which is then faster.
  *   prefix_table  int32 [ceil(prefix_len / 64)] (device; may be NULL when
  *                 prefix_len is 0)
  * A sequence with neither prefix nor own keys gets zeros.  Arithmetic as in
- * dvssq_bss_attention_q8, but over the prefix the query is FP16 (exact: scaled
- * by a power of two per head) and a weight is rounded once to FP16 (2^-12
- * relative).  Results are deterministic.
+ * dvssq_bss_attention_q8, but over a prefix that is read once the query is FP16
+ * (exact: scaled by a power of two per head) and a weight is rounded once to
+ * FP16 (2^-12 relative).  Results are deterministic.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, DEVICE, CUDA. */
 DVSSQ_API dvssq_status dvssq_bss_attention_prefix(const dvssq_attn_shape *shape,
                                                   const dvssq_kv_cache *cache,
