@@ -14,7 +14,7 @@
 // An item is a run of pages of one sequence and one KV head.  The lengths live
 // on the device, so every CTA derives the same plan from them: pages per item
 // such that the items fill whole rounds of the grid.
-// Contexts up to 64 pages take one launch instead (q8_short: a CTA, or a cluster of
+// Contexts up to 64 pages (q8_cluster) take one launch instead (q8_short: a CTA, or a cluster of
 // them, per sequence and KV head).
 //
 // Measured, 4 sequences of up to 32768 keys, 16/4 heads of 256 (190 MB of keys and
@@ -812,16 +812,17 @@ size_t q8_pv_smem(int NT, int B) {
 // pages the largest cluster that fits the resident CTAs, as long as a CTA gets at most 8
 // pages (16 of 64 dimensions, whose CTA needs less time per page); up to 32 pages 4 CTAs
 // also past that, unless 9 to 16 query heads leave room for one CTA per SM.  Beyond, three
-// launches spread ragged lengths better.  Measured in us (16/4 heads of 256; one launch with
+// launches spread ragged lengths better, but for few rows of 64 dimensions.  Measured in us (16/4 heads of 256; one launch with
 // 1 / 2 / 4 / 8 CTAs, three launches):
 //   1 x 100 keys 5.5 / 7.5 / 6.5 / 6.5, 9.6        16 x 4096   - / - / 34 / 28, 36
 //   1 x 1024     17.8 / 13.3 / 9.2 / 7.5, 10.2     1 x 8192    - / - / - / 19.8, 17.1
 //   16 x 1024    17.8 / 13.7 / 11.3 / 11.3, 18.1   64 x 1024   32 / 29 / 33 / 41, 36
 //   16 x <= 2048 - / 21.5 / 15.6 / 12.4, 17.5      148 x 1024  51 / 57 / 68 / 86, 64
-// 148 x 4096 of 16/2 heads of 128: - / - / 100 / 100, 87; of 8/8 heads of 64: - / - / 152 / 187, 186.
+// 148 x 4096 of 16/2 heads of 128: - / - / 100 / 100, 87; of 8/8 heads of 64: - / - / 152 / 187, 186;
+// 4 x 8192 of those - / - / - / 13.7, 18.4.
 int q8_cluster(const Q8Shape &s, int pages) {
-  if (pages > 64) return 0;
   const int NT = q8_tiles(s.Hq / s.Hkv), slots = kQ8Sms * q8_occ(NT), rows = s.B * s.Hkv;
+  if (pages > 64) return s.D == 64 && pages <= 8 * kQ8MaxPages && 8 * rows <= slots ? 8 : 0;
   const bool few = pages <= kQ8MaxPages;
   int C = 1;
   if (!few || (pages * s.D > 512 && 4 * rows <= slots))

@@ -273,13 +273,13 @@ def widened(dv, pool, table, width):
 @pytest.mark.parametrize("lens", [[1300, 64, 0, 1, 1025], [513, 0, 512], [2100], [3000, 3, 4096], [70] * 33 + [0, 900]],
                          ids=lambda x: f"B{len(x)}_{max(x)}")
 def test_every_form_of_every_head_layout(dv, Hq, H, d, lens):
-    """The same sequences with bounds of 1 x, 17, 33 and 65 pages: one CTA, clusters, three launches."""
+    """The same sequences with bounds of 1 x, 17, 33, 65 and 129 pages: one CTA, clusters, three launches."""
     B = len(lens)
     q = P.queries(B, Hq, d, seed=Hq + d)
     for bind, haze in ((None, 12.0), (14.0, 0.0)):
         pool, table, _ = P.filled(B, H, d, lens, seed=H + B, bind=bind and (q, bind))
         ref = P.attention(q, pool, table, lens, haze=haze)
-        for width in (0, 17, 33, 65):
+        for width in (0, 17, 33, 65, 129):
             c = widened(dv, pool, table, width)
             out = dv.dvssq_bss_attention_q8(q.cuda(), c, i32(lens), haze=haze)
             check(out, ref, DECODE)
