@@ -34,7 +34,7 @@
 // FP32-grade.  A weight is rounded once to FP16 (2^-12 relative), scaled by
 // 2^(14 - e) with 2^e at or above the head's largest vs: the rounding holds
 // down to e^-19 of the largest weight, and what underflows is below 2^-38 of it
-// (value scales of 2^-86 to 2^88; outside the weights lose bits towards either end).
+// (largest value scales from 2^-86; below, the weights lose bits).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -53,6 +53,7 @@ struct PfxParams {
   float *po;                     // [splits][H][rows][D]
   float *pl;                     // [splits][H][rows]
   uint32_t magic;                // 0x64646464
+  float nzero;                   // -0
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
@@ -181,32 +182,42 @@ __device__ __forceinline__ float pfx_half_max(const uint32_t *s, const float *ks
   return fmaxf(m0, m1);
 }
 
-// A row's weights of a quarter of a page (16 keys), FP16 pairs exp2(S ks r2 + x0) vs,
-// and the sum of the exponentials.  Whole: all the page's keys are live and no value scale is a NaN.  The two
+// A row's weights of a quarter of a page (16 keys), FP16 pairs exp2(t - m) (vs up), and
+// the sum of the exponentials.  t = (S ks) r2 is rounded as the maximum pass rounds it, and
+// only then does m come off: the largest key's difference is zero, however large the logits
+// are (fused into one operation it is the product's rounding error, which passes any
+// threshold and FP16's range in turn).  The second product is a packed FMA with `nzero`,
+// -0 from a kernel parameter: a packed multiplication before a packed addition is compiled
+// into one FMA, .rn or not.  `up`, the power of two that brings the weights into
+// FP16's range, goes with the value scale, so that the sum needs none.
+// Whole: all the page's keys are live and no value scale is a NaN.  The two
 // bodies are apart so that each is one straight block for the scheduler: with the
 // choice inside the loop 64 keys took 2700 cycles instead of 1700.
 template <bool Whole>
 __device__ __forceinline__ float2 pfx_weights16(const uint32_t *s, const float *ks, const float *vs,
-                                                   int nv, float r2, float x0, float floor2, uint32_t *w) {
-  const float2 rr = make_float2(r2, r2), xx = make_float2(x0, x0);
+                                                   int nv, float r2, float m, float haze2, float up, float nzero,
+                                                   uint32_t *w) {
+  const float2 rr = make_float2(r2, r2), nm = make_float2(-m, -m), uu = make_float2(up, up);
+  const float2 nz = make_float2(nzero, nzero);
   float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
     const float4 a = *reinterpret_cast<const float4 *>(ks + i);
     const float4 v = *reinterpret_cast<const float4 *>(vs + i);
-    const float2 x = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y)), rr, xx);
-    const float2 y = mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w)), rr, xx);
+    const float2 vx = mat_mul2(make_float2(v.x, v.y), uu), vy = mat_mul2(make_float2(v.z, v.w), uu);
+    const float2 x = mat_add2(mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y)), rr, nz), nm);
+    const float2 y = mat_add2(mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w)), rr, nz), nm);
     float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
     float2 ey = make_float2(ex2_approx(y.x), ex2_approx(y.y));
     float2 wx, wy;
     // below the haze threshold: dropped (a NaN logit is kept)
-    if (x.x < floor2) ex.x = 0.f;
-    if (x.y < floor2) ex.y = 0.f;
-    if (y.x < floor2) ey.x = 0.f;
-    if (y.y < floor2) ey.y = 0.f;
+    if (x.x < haze2) ex.x = 0.f;
+    if (x.y < haze2) ex.y = 0.f;
+    if (y.x < haze2) ey.x = 0.f;
+    if (y.y < haze2) ey.y = 0.f;
     if (Whole) {
-      wx = mat_mul2(ex, make_float2(v.x, v.y));
-      wy = mat_mul2(ey, make_float2(v.z, v.w));
+      wx = mat_mul2(ex, vx);
+      wy = mat_mul2(ey, vy);
     } else {
       // keys past the prefix's end weigh nothing, and the value scale of a key
       // without weight is not looked at
@@ -214,8 +225,8 @@ __device__ __forceinline__ float2 pfx_weights16(const uint32_t *s, const float *
       if (i + 1 >= nv) ex.y = 0.f;
       if (i + 2 >= nv) ey.x = 0.f;
       if (i + 3 >= nv) ey.y = 0.f;
-      wx = make_float2(ex.x == 0.f ? 0.f : ex.x * v.x, ex.y == 0.f ? 0.f : ex.y * v.y);
-      wy = make_float2(ey.x == 0.f ? 0.f : ey.x * v.z, ey.y == 0.f ? 0.f : ey.y * v.w);
+      wx = make_float2(ex.x == 0.f ? 0.f : ex.x * vx.x, ex.y == 0.f ? 0.f : ex.y * vx.y);
+      wy = make_float2(ey.x == 0.f ? 0.f : ey.x * vy.x, ey.y == 0.f ? 0.f : ey.y * vy.y);
     }
     sum = mat_add2(sum, mat_add2(ex, ey));
     const __half2 ox = __floats2half2_rn(wx.x, wx.y), oy = __floats2half2_rn(wy.x, wy.y);
@@ -372,23 +383,20 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     const int b = live ? rr / G : 0, hq = h * G + (live ? rr - b * G : 0);
     const float r2 = s_step[row] * p.q8.scale2;      // logit (in units of log2 e) = S ks r2
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    float mx = -INFINITY, x0 = 0.f, floor2 = -INFINITY;
+    float mx = -INFINITY, m = 0.f, up = 1.f;
     float2 sum = make_float2(0.f, 0.f);
     int shift = 0;
     if constexpr (PV) {
       pdl_wait();                                    // the row maxima, over the prefix and the own keys
-      const float m = *(volatile float *)&p.q8.mfin[(size_t)b * p.q8.Hq + hq];
-      // weights times 2^shift: the largest vs 2^shift lies in [2^13, 2^14)
+      m = q8_reference(*(volatile float *)&p.q8.mfin[(size_t)b * p.q8.Hq + hq], false);
+      // value scales times 2^shift: the largest lies in [2^13, 2^14)
       const float sv = *(volatile float *)&p.q8.svfin[h];
       if (sv > 0.f) {
         int e;
         frexpf(sv, &e);                              // vs < 2^e
-        shift = min(14 - e, 100);                    // (the sum of a long prefix stays finite)
+        shift = min(14 - e, 100);                    // (taken back, FP16's smallest stays normal in FP32)
       }
-      if (m > -INFINITY) {
-        x0 = (float)shift - m;                       // exponent of a weight: S ks r2 + x0
-        floor2 = (float)shift + p.q8.haze2;
-      }
+      up = ldexpf(1.0f, shift);
     }
     for (int j = 0; j < n && ok; ++j) {
       const int sb = j & 3, ss = j % NS;
@@ -411,9 +419,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
         for (int c = 0; c < 2; ++c) {
           uint32_t w[8];
           if (whole)
-            sum = mat_add2(sum, pfx_weights16<true>(s + 16 * c, ks + 16 * c, vs + 16 * c, 16, r2, x0, floor2, w));
+            sum = mat_add2(sum, pfx_weights16<true>(s + 16 * c, ks + 16 * c, vs + 16 * c, 16, r2, m, p.q8.haze2, up, p.nzero, w));
           else
-            sum = mat_add2(sum, pfx_weights16<false>(s + 16 * c, ks + 16 * c, vs + 16 * c, live_keys - 16 * c, r2, x0, floor2, w));
+            sum = mat_add2(sum, pfx_weights16<false>(s + 16 * c, ks + 16 * c, vs + 16 * c, live_keys - 16 * c, r2, m, p.q8.haze2, up, p.nzero, w));
           tmem_st8(src + 8 * c, w);                  // over this thread's S
         }
         tmem_st_wait();
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       // the last weights were waited for)
       if (wg == 1) s_step[row] = sum.x + sum.y;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (wg == 0 && live) p.pl[at + rr] = (sum.x + sum.y + s_step[row]) * back;
+      if (wg == 0 && live) p.pl[at + rr] = sum.x + sum.y + s_step[row];
       // each warpgroup half of the columns, 32 x 32 blocks through shared memory (the
       // ring, free now): whole 128-byte lines out
       float (*st)[36] = reinterpret_cast<float (*)[36]>(pfx_sm + warp * 32 * 36 * 4);
@@ -706,6 +714,7 @@ cudaError_t launch_prefix_attention(const Q8Args &a, cudaStream_t st, Launcher &
   p.q8 = q8_params(a, y.q8);
   p.ptable = a.ptable;
   p.magic = 0x64646464u;
+  p.nzero = -0.0f;
   p.prefix = a.s.prefix; p.pages = y.pages; p.splits = y.splits; p.rows = y.rows;
   p.pmax = reinterpret_cast<float *>(ws + y.pmax);
   p.psv = reinterpret_cast<float *>(ws + y.psv);
