@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       ahead = page_id(t + kPfxConv);
       nv = min(64, p.prefix - 64 * (j0 + page_of(t)));
       if (page < 0 || page >= p.q8.n_pages) {        // its keys weigh nothing
-        set_error(kErrBadIndex);
+        set_index_error();
         page = nv = 0;
       }
       const size_t ph = (size_t)page * H + h;

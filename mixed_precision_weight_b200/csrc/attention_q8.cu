@@ -70,7 +70,7 @@ struct Q8Params {
 
 __device__ __forceinline__ int q8_len(const Q8Params &p, int b) {
   const int n = p.lens[b];
-  if (n < 0 || n > p.ctx) set_error(kErrBadIndex);
+  if (n < 0 || n > p.ctx) set_index_error();
   return max(0, min(n, p.ctx));
 }
 
@@ -226,7 +226,7 @@ __device__ __forceinline__ void q8_pages(const Q8Params &p, Q8Shared<D, NT> &sm,
     int x = w < 0 ? p.ptable[at] : p.table[(size_t)b * p.W + w];
     int n = w < 0 ? p.prefix - 64 * at : len - 64 * w;
     if (x < 0 || x >= p.n_pages) {
-      set_error(kErrBadIndex);
+      set_index_error();
       x = -1;
       n = 0;
     }

@@ -661,11 +661,15 @@ dvssq_status dvssq_device_error(uint32_t *word, int32_t clear) {
   if (word == nullptr) return DVSSQ_ERR_INVALID_ARG;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e);
-  if ((e = cudaMemcpyFromSymbol(word, g_dvssq_error, sizeof(uint32_t))) != cudaSuccess)
+  uint32_t index = 0;
+  if ((e = cudaMemcpyFromSymbol(word, g_dvssq_error, sizeof(uint32_t))) != cudaSuccess ||
+      (e = cudaMemcpyFromSymbol(&index, g_dvssq_index_error, sizeof(uint32_t))) != cudaSuccess)
     return cuda_fail(e);
+  *word |= index;
   if (clear) {
     const uint32_t z = 0;
-    if ((e = cudaMemcpyToSymbol(g_dvssq_error, &z, sizeof(uint32_t))) != cudaSuccess)
+    if ((e = cudaMemcpyToSymbol(g_dvssq_error, &z, sizeof(uint32_t))) != cudaSuccess ||
+        (e = cudaMemcpyToSymbol(g_dvssq_index_error, &z, sizeof(uint32_t))) != cudaSuccess)
       return cuda_fail(e);
   }
   return DVSSQ_OK;

@@ -229,6 +229,11 @@ cudaError_t launch_bss_attention(const BssArgs &a, cudaStream_t st, Launcher &L)
 // ------------------------------------------------------------ 8-bit KV cache -
 // Bit of the device error word: an index (page, position, length, row) out of range.
 constexpr uint32_t kErrBadIndex = 1u << 4;
+// Kept in a word of its own, which dvssq_device_error adds to the others: a grid barrier
+// (counter_wait) gives up when its word changes, and a skipped index is no reason for a
+// kernel on another stream to do so.
+__device__ uint32_t g_dvssq_index_error = 0;
+__device__ __forceinline__ void set_index_error() { atomicOr(&g_dvssq_index_error, kErrBadIndex); }
 // The pool of pages and the sequences' page table (device pointers).
 struct KvPool {
   int8_t *k, *v;

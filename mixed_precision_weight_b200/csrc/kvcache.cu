@@ -79,21 +79,21 @@ __device__ __forceinline__ bool kv_find_run(const KvIndex &ix, int item, KvRun &
   bool bad = false;
   if (row0 < 0 || row0 + n > ix.T) {
     bad = true;
-    if (row0 < 0) return set_error(kErrBadIndex), false;
+    if (row0 < 0) return set_index_error(), false;
     n = ix.T - row0;
-    if (n <= 0) return set_error(kErrBadIndex), false;
+    if (n <= 0) return set_index_error(), false;
   }
-  if (pos < 0) return set_error(kErrBadIndex), false;
+  if (pos < 0) return set_index_error(), false;
   const long long p = (pos >> 6) + j;
   const long long a = max(pos, 64 * p), z = min(pos + n, 64 * (p + 1));
   if (a >= z) {
-    if (bad) set_error(kErrBadIndex);
+    if (bad) set_index_error();
     return false;
   }
-  if (p >= ix.W) return set_error(kErrBadIndex), false;
+  if (p >= ix.W) return set_index_error(), false;
   r.page = ix.table[(size_t)b * ix.W + p];
-  if (r.page < 0 || r.page >= ix.n_pages) return set_error(kErrBadIndex), false;
-  if (bad) set_error(kErrBadIndex);
+  if (r.page < 0 || r.page >= ix.n_pages) return set_index_error(), false;
+  if (bad) set_index_error();
   r.row0 = row0 + (a - pos);
   r.slot0 = (int)(a - 64 * p);
   r.n = (int)(z - a);
