@@ -341,10 +341,11 @@ DVSSQ_API dvssq_status dvssq_bss_attention(const dvssq_attn_shape *shape, const 
  * Indices live on the device, so the kernels check them: a page id outside
  * the pool, a position outside the table, a row outside the call's rows or a
  * length outside [0, ctx] sets bit 4 of the device error word
- * (dvssq_device_error); the row is then skipped, the page's keys are left out
- * of the attention, the length is clamped, and nothing out of range is read
- * or written.  Two rows of one call that land on the same slot (sequences
- * that share a page) leave that slot undefined.                             */
+ * (dvssq_device_error); the row is then skipped (its neighbours are not,
+ * unless their sequence begins before the call's first row), the page's keys
+ * are left out of the attention, the length is clamped, and nothing out of
+ * range is read or written.  Two rows of one call that land on the same slot
+ * (sequences that share a page) leave that slot undefined.                  */
 #define DVSSQ_KV_PAGE 64
 typedef struct {
   int8_t *k;

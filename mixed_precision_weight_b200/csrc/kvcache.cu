@@ -47,9 +47,9 @@ struct KvRun {
 // 2 (b+1)): n rows touch at most n / 64 + 2 pages, so that range covers them
 // without a prefix sum, and a warp-wide search over cu finds b (its last round reads
 // the start positions along, so that a call on up to 31 sequences waits for two
-// loads before its rows: these and the page's id).  Rows outside [0, T), positions
-// outside the table and pages outside the pool are skipped and flagged.  Whole
-// warps call this; false: nothing to do.
+// loads before its rows: these and the page's id).  Rows at and past T, sequences that
+// begin before row 0, positions outside the table and pages outside the pool are
+// skipped and flagged.  Whole warps call this; false: nothing to do.
 __device__ __forceinline__ bool kv_find_run(const KvIndex &ix, int item, KvRun &r) {
   const int lane = threadIdx.x & 31;
   int b = item, j = 0;
@@ -83,14 +83,13 @@ __device__ __forceinline__ bool kv_find_run(const KvIndex &ix, int item, KvRun &
     n = ix.T - row0;
     if (n <= 0) return set_index_error(), false;
   }
-  if (pos < 0) return set_index_error(), false;
   const long long p = (pos >> 6) + j;
   const long long a = max(pos, 64 * p), z = min(pos + n, 64 * (p + 1));
   if (a >= z) {
     if (bad) set_index_error();
     return false;
   }
-  if (p >= ix.W) return set_index_error(), false;
+  if (p < 0 || p >= ix.W) return set_index_error(), false;
   r.page = ix.table[(size_t)b * ix.W + p];
   if (r.page < 0 || r.page >= ix.n_pages) return set_index_error(), false;
   if (bad) set_index_error();
