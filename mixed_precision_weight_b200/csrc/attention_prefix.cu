@@ -164,16 +164,18 @@ __device__ __forceinline__ bool pfx_wait(uint64_t *bar, uint32_t parity, long lo
   return true;
 }
 
-// A row's 32 products of half a page: their largest logit over ks (a NaN is passed over).
+// A row's 32 products of half a page: their largest logit S (ks r2) (a NaN is passed over).
+// The two scales first: their product lies near the logit, S times either may pass FP32's range.
 // Whole: all the page's keys are live; else the half's first nv are.
 template <bool Whole>
-__device__ __forceinline__ float pfx_half_max(const uint32_t *s, const float *ks, int nv) {
+__device__ __forceinline__ float pfx_half_max(const uint32_t *s, const float *ks, int nv, float r2) {
+  const float2 rr = make_float2(r2, r2);
   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 a = *reinterpret_cast<const float4 *>(ks + i);
-    const float2 x = mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y));
-    const float2 y = mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w));
+    const float2 x = mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), mat_mul2(make_float2(a.x, a.y), rr));
+    const float2 y = mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), mat_mul2(make_float2(a.z, a.w), rr));
     if (Whole || i < nv) m0 = fmaxf(m0, x.x);
     if (Whole || i + 1 < nv) m0 = fmaxf(m0, x.y);
     if (Whole || i + 2 < nv) m1 = fmaxf(m1, y.x);
@@ -183,7 +185,7 @@ __device__ __forceinline__ float pfx_half_max(const uint32_t *s, const float *ks
 }
 
 // A row's weights of a quarter of a page (16 keys), FP16 pairs exp2(t - m) (vs up), and
-// the sum of the exponentials.  t = (S ks) r2 is rounded as the maximum pass rounds it, and
+// the sum of the exponentials.  t = S (ks r2) is rounded as the maximum pass rounds it, and
 // only then does m come off: the largest key's difference is zero, however large the logits
 // are (fused into one operation it is the product's rounding error, which passes any
 // threshold and FP16's range in turn).  The second product is a packed FMA with `nzero`,
@@ -205,8 +207,8 @@ __device__ __forceinline__ float2 pfx_weights16(const uint32_t *s, const float *
     const float4 a = *reinterpret_cast<const float4 *>(ks + i);
     const float4 v = *reinterpret_cast<const float4 *>(vs + i);
     const float2 vx = mat_mul2(make_float2(v.x, v.y), uu), vy = mat_mul2(make_float2(v.z, v.w), uu);
-    const float2 x = mat_add2(mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(a.x, a.y)), rr, nz), nm);
-    const float2 y = mat_add2(mat_fma2(mat_mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(a.z, a.w)), rr, nz), nm);
+    const float2 x = mat_add2(mat_fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), mat_mul2(make_float2(a.x, a.y), rr), nz), nm);
+    const float2 y = mat_add2(mat_fma2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), mat_mul2(make_float2(a.z, a.w), rr), nz), nm);
     float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
     float2 ey = make_float2(ex2_approx(y.x), ex2_approx(y.y));
     float2 wx, wy;
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
     const int row = tid & 127, rr = rt * 128 + row;
     const bool live = rr < p.rows;
     const int b = live ? rr / G : 0, hq = h * G + (live ? rr - b * G : 0);
-    const float r2 = s_step[row] * p.q8.scale2;      // logit (in units of log2 e) = S ks r2
+    const float r2 = s_step[row] * p.q8.scale2;      // logit (in units of log2 e) = S (ks r2)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float mx = -INFINITY, m = 0.f, up = 1.f;
     float2 sum = make_float2(0.f, 0.f);
@@ -411,8 +413,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       tmem_ld32(src, s);
       tmem_ld_wait32(s);
       if constexpr (!PV) {
-        if (nv == 64) mx = fmaxf(mx, pfx_half_max<true>(s, ks, live_keys));
-        else mx = fmaxf(mx, pfx_half_max<false>(s, ks, live_keys));
+        if (nv == 64) mx = fmaxf(mx, pfx_half_max<true>(s, ks, live_keys, r2));
+        else mx = fmaxf(mx, pfx_half_max<false>(s, ks, live_keys, r2));
       } else {
         const bool whole = nv == 64 && s_nv[sb][1] == 0;
 #pragma unroll
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) pfx_kernel(const PfxParams p) 
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (wg == 1) s_step[row] = mx;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (wg == 0 && live) p.pmax[((size_t)split * H + h) * p.rows + rr] = fmaxf(mx, s_step[row]) * r2;
+      if (wg == 0 && live) p.pmax[((size_t)split * H + h) * p.rows + rr] = fmaxf(mx, s_step[row]);
     } else {
       if (!__all_sync(0xffffffffu, ok && pfx_wait(o_full, 0, limit))) ok = false;
       tc_fence_after();

@@ -316,9 +316,10 @@ __device__ __forceinline__ void q8_logits_run(const Q8Params &p, Q8Shared<D, NT>
       const bool v0 = key < live, v1 = key + 8 < live;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        // 256 hi + lo in exact integers, rounded once to FP32
-        const float l0 = v0 ? (float)(acc[nt][0] * 256 + acc[nt][1]) * k0 * step[nt] : -INFINITY;
-        const float l1 = v1 ? (float)(acc[nt][2] * 256 + acc[nt][3]) * k1 * step[nt] : -INFINITY;
+        // 256 hi + lo in exact integers, rounded once to FP32.  The two scales first: their
+        // product lies near the logit, the sum times either may pass FP32's range
+        const float l0 = v0 ? (float)(acc[nt][0] * 256 + acc[nt][1]) * (k0 * step[nt]) : -INFINITY;
+        const float l1 = v1 ? (float)(acc[nt][2] * 256 + acc[nt][3]) * (k1 * step[nt]) : -INFINITY;
         put(at, 4 * nt + tig, l0);
         put(at + 8, 4 * nt + tig, l1);
         float m = max_nan(l0, l1);

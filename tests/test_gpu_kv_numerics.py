@@ -113,3 +113,29 @@ def test_equal_largest_keys_in_prefix_and_own_part(dv, tau):
     ref = P.attention(q, pool, table, lens, tau=tau, ptable=ptable, prefix=prefix)
     out = dv.dvssq_bss_attention_prefix(q.cuda(), c, i32(lens), ptable.cuda(), prefix, tau=tau)
     check(out, ref, PREFIX)
+
+
+@pytest.mark.parametrize("up", [111, -111, 60, -60])
+@pytest.mark.parametrize("Hq,H,d", [(8, 8, 64), (16, 2, 128), (16, 1, 128), (16, 4, 256)])
+def test_ordinary_logits_of_huge_and_tiny_factors(dv, Hq, H, d, up):
+    """Keys times 2^up and queries times 2^-up: the logits are those of neither, bit for bit in exact
+    arithmetic, so that the bounds are the ordinary ones."""
+    lens = [1300, 64, 1, 0, 700, 130, 65]
+    q = P.queries(7, Hq, d, seed=d)
+    prefix = 64 * ((4096 if Hq // H <= 8 else 2400) // (7 * H) + 1) - 27
+    pool, table, ptable = P.filled(7, H, d, lens, seed=d + 1, prefix=prefix)
+    ref = P.attention(q, pool, table, lens)
+    both = P.attention(q, pool, table, lens, ptable=ptable, prefix=prefix)
+    pool["ks"] = (pool["ks"].float() * 2.0 ** up).to(torch.bfloat16)
+    assert not pool["ks"].isinf().any()
+    qg = (q.float() * 2.0 ** -up).to(torch.bfloat16).cuda()
+    assert torch.equal(qg.cpu().double() * 2.0 ** up, q.double())           # no bit was lost
+    for width in (0, 33, 130):
+        check(dv.dvssq_bss_attention_q8(qg, widened(dv, pool, table, width), i32(lens)), ref, DECODE)
+    for width in (0, 17):
+        c = widened(dv, pool, table, width)
+        check(dv.dvssq_bss_attention_prefix(qg, c, i32(lens), ptable.cuda(), prefix), both, PREFIX)
+    c = widened(dv, pool, table, 0)
+    few = P.attention(q, pool | {"ks": (pool["ks"].float() * 2.0 ** -up).to(torch.bfloat16)}, table, lens,
+                      ptable=ptable, prefix=100)
+    check(dv.dvssq_bss_attention_prefix(qg, c, i32(lens), ptable[:2].cuda(), 100), few, DECODE)
