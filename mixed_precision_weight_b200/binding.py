@@ -379,10 +379,11 @@ def dvssq_bss_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tau: 
 KV_PAGE = 64
 
 # The calls below sit in decode loops of a few microseconds: they read the current
-# device and stream without building torch objects, and keep the checks to plain
-# attribute reads.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# device and stream without building torch objects (where this torch has those reads,
+# which are not public), and keep the checks to plain attribute reads.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _on:
