@@ -206,3 +206,72 @@ def test_captured_calls_read_their_inputs_anew(dv, kind):
         lens.copy_(torch.tensor(c.lens, dtype=torch.int32))
         g.replay()
         check(out, c.ref(), c.bound)
+
+
+# --------------------------------------------------------------- largest counts ---
+def some(c, at):
+    """The plain result of sequences `at` alone."""
+    lens = [c.lens[i] for i in at]
+    if isinstance(c, Prefix):
+        return P.attention(c.q[at], c.pool, c.table[at], lens, haze=c.haze, ptable=c.ptable, prefix=c.prefix)
+    return P.attention(c.q[at], c.pool, c.table[at], lens, haze=c.haze)
+
+
+def test_three_launches_over_4096_sequences(dv):
+    c = Decode(dv, 2, 1, 64, [(i * 7) % 71 for i in range(4096)], seed=61)
+    out = c()
+    check(out, c.ref(), DECODE)
+    assert (out[::71] == 0).all()
+
+
+def test_prefix_read_once_by_4096_sequences_of_16_heads(dv):
+    """65536 rows per KV head: 512 row tiles, more than the SMs; one split."""
+    c = Prefix(dv, 16, 1, 64, [i % 3 for i in range(4096)], 130, 62, False)
+    check(c(), c.ref(), PREFIX)
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_1024_kv_heads(dv, split):
+    lens = [1, 0, 70]
+    c = Prefix(dv, 1024, 1024, 64, lens, 140, 63, split)
+    check(c(), c.ref(), PREFIX)
+    d = Decode(dv, 1024, 1024, 64, lens, 64)
+    check(d(), d.ref(), DECODE)
+
+
+@pytest.mark.parametrize("prefix", [9000, 32768])
+def test_one_split_of_a_long_prefix(dv, prefix):
+    """So many rows that a CTA walks the whole prefix."""
+    c = Prefix(dv, 7, 7, 128, [i % 2 for i in range(2500)], prefix, 65, False)
+    at = [0, 1, 777, 1500, 2499]
+    check(c()[at], some(c, at), PREFIX)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_append_and_read_over_4096_sequences(dv, d):
+    B, H = 4096, 1
+    g = torch.Generator().manual_seed(d)
+    n = torch.randint(0, 4, (B,), generator=g)
+    n[100], n[4095] = 300, 129
+    start = torch.randint(0, 200, (B,), generator=g)
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), n.cumsum(0)])
+    T, W = int(cu[-1]), 8
+    table = torch.randperm(B * W, generator=g).to(torch.int32).reshape(B, W)
+    pool = dict(k=torch.zeros((B * W, H, 64, d), dtype=torch.int8), v=torch.zeros((B * W, H, d, 64), dtype=torch.int8),
+                ks=torch.zeros((B * W, H, 64), dtype=torch.bfloat16), vs=torch.zeros((B * W, H, 64), dtype=torch.bfloat16))
+    k, v = (torch.randn((T, H, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    c = to_gpu(dv, pool, table)
+    sg, cg = i32(start.tolist()), i32(cu.tolist())
+    dv.dvssq_kv_append(c, k.cuda(), v.cuda(), sg, cg)
+    b = torch.repeat_interleave(torch.arange(B), n)
+    pos = start[b] + torch.arange(T) - cu[b]
+    page, slot = table[b, pos // 64].long(), pos % 64
+    kc, ks = P.hold(k)
+    vc, vs = P.hold(v)
+    pool["k"][page, :, slot], pool["ks"][page, :, slot] = kc, ks
+    pool["v"][page, :, :, slot], pool["vs"][page, :, slot] = vc, vs
+    assert torch.equal(c.k.cpu(), pool["k"]) and torch.equal(c.v.cpu(), pool["v"])
+    assert torch.equal(c.k_scale.cpu(), pool["ks"]) and torch.equal(c.v_scale.cpu(), pool["vs"])
+    ko, vo = dv.dvssq_kv_read(c, sg, cg, T)
+    assert torch.equal(ko.cpu(), (kc.float() * ks.float()[..., None]).to(torch.bfloat16))
+    assert torch.equal(vo.cpu(), (vc.float() * vs.float()[..., None]).to(torch.bfloat16))
