@@ -405,13 +405,19 @@ DVSSQ_API dvssq_status dvssq_bss_attention_q8_workspace_size(const dvssq_attn_sh
  *   lens    int32 [batch] (device); a sequence of length 0 gets zeros
  *   out     [batch][q_heads][head_dim] (device), fp32 or bf16 by y_dtype
  *           (DVSSQ_Y_*; bf16 rounds the fp32 result to nearest even)
- * The query enters as 16-bit integers of a power-of-two step per head, exact
- * for values down to 2^-8 of the head's largest magnitude (smaller ones are
- * off by at most 2^-15 of it); q . k is then exact, logits, maxima,
- * exponentials and sums are FP32, and a weight times its value scale enters
- * P V as two BF16 limbs (2^-17 relative).  A key whose weight is zero adds
- * nothing, whatever its value scale holds; a NaN key row makes its KV head's
- * outputs NaN.  tau is at most 1e30.  Results are deterministic.
+ * The query enters as 16-bit integers of the step 2^(e-14) per head, 2^e the
+ * power of two at or below the head's largest magnitude: exact from 2^(e-7)
+ * on, but for +255/128 2^e, which is one step low; smaller values are off by
+ * half a step at most, so that a head of one large value beside small ones
+ * keeps few bits of those.  The product of these integers with the codes is
+ * exact; logits (NaN past FP32's range), maxima, exponentials and sums are
+ * FP32, and a weight times its value scale enters P V as two BF16 limbs
+ * (2^-17 relative).  A key whose weight is zero adds nothing, whatever its
+ * value scale holds; a NaN key row makes its KV head's outputs NaN.  tau is
+ * at most 1e30.  Results are deterministic.
+ * The kernels are chosen by ctx, not by the lengths: a bound near them (a
+ * captured step's: near its longest) is faster than a table's capacity.
+ * 17 keys take 5 us under their own bound, 10 us under one of 8192.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, DEVICE, CUDA. */
 DVSSQ_API dvssq_status dvssq_bss_attention_q8(const dvssq_attn_shape *shape,
                                               const dvssq_kv_cache *cache, const void *q,
@@ -437,8 +443,11 @@ DVSSQ_API dvssq_status dvssq_bss_attention_prefix_workspace_size(const dvssq_att
  *                 prefix_len is 0)
  * A sequence with neither prefix nor own keys gets zeros.  Arithmetic as in
  * dvssq_bss_attention_q8, but over a prefix that is read once the query is FP16
- * (exact: scaled by a power of two per head) and a weight is rounded once to
- * FP16 (2^-12 relative).  Results are deterministic.
+ * (exact: scaled by a power of two per head) and a weight times its value scale
+ * is rounded once to FP16: 2^-11 relative, as long as it is above 2^-27 of the
+ * prefix's largest value scale of the KV head (a key's that the row may have
+ * dropped); below that it is off by up to 2^-38 of that scale.  Results are
+ * deterministic.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, DEVICE, CUDA. */
 DVSSQ_API dvssq_status dvssq_bss_attention_prefix(const dvssq_attn_shape *shape,
                                                   const dvssq_kv_cache *cache,

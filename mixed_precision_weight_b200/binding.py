@@ -638,7 +638,8 @@ def dvssq_bss_attention_q8(q: torch.Tensor, cache: KvCache, lens: torch.Tensor, 
     """KV-BSS decode attention over the 8-bit cache: q [B][Hq][d] (BF16) -> [B][Hq][d].
 
     ``lens`` int32 [B]: each sequence's keys; ``ctx``: an upper bound on them
-    (the table's capacity when left out), which sizes the workspace.
+    (the table's capacity when left out), which sizes the workspace and chooses
+    the kernels: a bound near the lengths is faster.
     """
     if stream is not None or _current_device() != cache.index:
         with _on(cache.index, stream):

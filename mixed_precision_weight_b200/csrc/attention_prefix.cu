@@ -23,15 +23,15 @@
 //
 // Measured, 64 sequences of 16/4 heads of 256 over 32768 keys (34.5 GFLOP and 88 MB: floor
 // 21 us of tensor rate, 31 with the second Q K^T): 85 us in a graph, of which maximum pass
-// 24, weight pass 45, own keys and merge the rest.  A page takes about 2300 cycles in the
+// 24, weight pass 46, own keys and merge the rest.  A page takes about 2300 cycles in the
 // weight pass against 1024 of products: the converting warps' loads, conversions and
 // shared-memory stores bound it (the load-store pipe is busy 50 % of the time, the
-// schedulers 55 %, the tensor pipe 37 %).
+// schedulers 56 %, the tensor pipe 37 %).
 //
 // Number formats: a code is exact in FP16 (1024 + u from a byte permutation,
 // minus 1152), and so is a query scaled by a power of two to 2^14 .. 2^15 (BF16
 // has 8 significant bits; values 2^29 below the row's largest vanish), so S is
-// FP32-grade.  A weight is rounded once to FP16 (2^-12 relative), scaled by
+// FP32-grade.  A weight is rounded once to FP16 (2^-11 relative), scaled by
 // 2^(14 - e) with 2^e at or above the head's largest vs: the rounding holds
 // down to e^-19 of the largest weight, and what underflows is below 2^-38 of it
 // (largest value scales from 2^-86; below, the weights lose bits).

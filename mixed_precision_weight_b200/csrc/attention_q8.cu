@@ -21,7 +21,7 @@
 // values, 29 us at copy bandwidth; the L2 keeps part of them from call to call): 44 us in a
 // graph, of which logits 18 (5.3 TB/s), P V 21 (4.5 TB/s), merge 3.  Neither pass
 // saturates anything: four CTAs of 128 threads per SM (120 registers hold the pages in
-// flight) issue on 20 and 36 % of the cycles and wait for their rows, after a prologue (plan,
+// flight) issue on 19 and 37 % of the cycles and wait for their rows, after a prologue (plan,
 // page ids, query or maxima) of about 3 us.
 #include "common.cuh"
 #include "kernels.h"
@@ -165,8 +165,10 @@ __device__ __forceinline__ uint32_t word(const uint4 &u, int i) {
 }
 
 // One query head as limbs: 16-bit integers of step 2^(e - 14), e the exponent of
-// the head's largest magnitude (exact for BF16 values of the top 8 binades,
-// off by at most one unit below); hi and lo rows of bytes.  A whole warp.
+// the head's largest magnitude: exact for BF16 values of the top 8 binades (but for
+// +255/128 2^e, one unit more than two signed bytes hold), off by half a unit at most
+// below; hi and lo rows of bytes.  Two limbs because four heads of two fill the eight
+// columns of a product.  A whole warp.
 template <int D>
 __device__ __forceinline__ void q8_limbs(const uint16_t *q, int8_t *hi, int8_t *lo, float *step) {
   constexpr int VPL = D / 32;
@@ -186,7 +188,7 @@ __device__ __forceinline__ void q8_limbs(const uint16_t *q, int8_t *hi, int8_t *
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const uint32_t bits = i & 1 ? raw.w[i / 2] >> 16 : raw.w[i / 2] & 0xFFFFu;
-    // the clamp only meets the mantissa 255/128, one unit above hi = lo = 127
+    // the clamp only meets +255/128 2^e, one unit above hi = lo = 127
     const int x = finite ? min(__float2int_rn(bf16_bits_to_f32(bits) * f0 * f1), 32639) : 0;
     const int l = ((x + 128) & 255) - 128;
     pl[i / 4] |= ((uint32_t)l & 0xFFu) << (8 * (i & 3));
@@ -842,6 +844,8 @@ int q8_cluster(const Q8Shape &s, int pages) {
 //   16/2 of 128: 24 x 5001 (3792) 24 / 25, 48 x 3000 (4512) 27 / 26; 8/8 of 64: 24 x 1900
 //   (5760) 15 / 20, 24 x 3000 (9024) 24 / 21; 32/2 of 256: 16 x 5001 (2528) 34 / 36,
 //   48 x 1900 (2880) 38 / 38, 8 x 16000 (4000) 46 / 38.
+// The rule is a compromise: it counts visits, not a page's bytes, and of 64 dimensions the
+// joined form is ahead up to about 8000 visits (2 x 32768 keys 25 / 47), which it leaves.
 bool q8_joins(const Q8Shape &s) {
   const long long rows = (long long)s.B * s.Hkv, pages = (s.prefix + 63) / 64;
   return s.prefix > 0 && rows * pages <= (s.Hq / s.Hkv <= 8 ? 4096 : 2400) &&

@@ -129,12 +129,12 @@ __device__ __forceinline__ KvRaw<VPL> kv_load(const uint16_t *src) {
 }
 
 // One row held by a warp -> its scale (BF16 bits) and this lane's VPL codes as bytes.
-// x / s is the reciprocal's quotient with one residual step, exact for these 8-bit
-// significands, and no larger than 127 (1 + 2^-8), so that rounding needs no clamp;
-// adding 1.5 2^23 rounds it to the nearest integer, ties to even, and leaves the
-// code in the low byte.  Two values at a time (packed FP32).  Where the residual
-// could fall below the normal range (s < 1e-27): the plain division, and a clamp,
-// because the scale itself may be a subnormal.
+// x / s is the reciprocal's quotient with one residual step (Markstein's correction:
+// q + r (x - q s) by two FMAs), exact for these 8-bit significands, and no larger than
+// 127 (1 + 2^-8), so that rounding needs no clamp; adding 1.5 2^23 rounds it to the
+// nearest integer, ties to even, and leaves the code in the low byte.  Two values at a
+// time (packed FP32).  Where the residual could fall below the normal range (s < 1e-27):
+// the plain division, and a clamp, because the scale itself may be a subnormal.
 template <int VPL>
 __device__ __forceinline__ uint32_t kv_quantise(const KvRaw<VPL> &raw, uint32_t *codes) {
   // the largest magnitude by its bits: a NaN or an infinity stays the largest
