@@ -327,7 +327,8 @@ DVSSQ_API dvssq_status dvssq_bss_attention(const dvssq_attn_shape *shape, const 
  * tier (Spark card, Tier A), one BF16 scale per row:
  *   s = RN_bf16(max|x| / 127),  c = clip(rint(x / s), -127, 127)  (0 if s = 0)
  * and stands for c s.  A row with an infinity or a NaN gets a NaN scale and
- * reads back as NaN.
+ * reads back as NaN; c s may pass BF16's range where max|x| is within 2^-8 of
+ * its end.
  *
  * The pool holds n_pages pages of DVSSQ_KV_PAGE tokens each:
  *   k        int8 [n_pages][kv_heads][64][head_dim]
@@ -410,8 +411,8 @@ DVSSQ_API dvssq_status dvssq_bss_attention_q8_workspace_size(const dvssq_attn_sh
  * on, but for +255/128 2^e, which is one step low; smaller values are off by
  * half a step at most, so that a head of one large value beside small ones
  * keeps few bits of those.  The product of these integers with the codes is
- * exact; logits (NaN past FP32's range), maxima, exponentials and sums are
- * FP32, and a weight times its value scale enters P V as two BF16 limbs
+ * exact; logits (NaN past FP32's range), maxima, exponentials and sums (of
+ * weights times values, divided at the end) are FP32, and a weight times its value scale enters P V as two BF16 limbs
  * (2^-17 relative).  A key whose weight is zero adds nothing, whatever its
  * value scale holds; a NaN key row makes its KV head's outputs NaN.  tau is
  * at most 1e30.  Results are deterministic.

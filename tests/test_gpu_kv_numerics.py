@@ -139,3 +139,29 @@ def test_ordinary_logits_of_huge_and_tiny_factors(dv, Hq, H, d, up):
     few = P.attention(q, pool | {"ks": (pool["ks"].float() * 2.0 ** -up).to(torch.bfloat16)}, table, lens,
                       ptable=ptable, prefix=100)
     check(dv.dvssq_bss_attention_prefix(qg, c, i32(lens), ptable[:2].cuda(), 100), few, DECODE)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_extreme_rows_read_back_exactly(dv, d):
+    """Rows from the smallest subnormal to the largest BF16 value: every value read back is the exact
+    product of its code and scale, rounded once (subnormal results among them)."""
+    g = torch.Generator().manual_seed(d)
+    exps = [-133, -130, -127, -126, -125, -120, -110, -95, -90, -60, 0, 60, 100, 120, 124, 125]
+    x = torch.stack([(torch.randn(1, d, generator=g) * 2.0 ** (e / 2)).to(torch.bfloat16).float() * 2.0 ** (e - e / 2)
+                     for e in exps]).clamp(-3.3895313892515355e38, 3.3895313892515355e38).to(torch.bfloat16)
+    x[-1, 0, :2] = torch.tensor([3.3895313892515355e38, -3.3895313892515355e38]).to(torch.bfloat16)
+    T = len(exps)
+    pool, table, _ = P.filled(1, 1, d, [T], seed=d)
+    pool["ks"].nan_to_num_(0.0)
+    pool["vs"].nan_to_num_(0.0)
+    c = to_gpu(dv, pool, table)
+    P.append(pool, table, x, x.flip(0), [0], [0, T])
+    dv.dvssq_kv_append(c, x.cuda(), x.flip(0).contiguous().cuda(), i32([0]), i32([0, T]))
+    assert torch.equal(c.k_scale.cpu(), pool["ks"]) and torch.equal(c.v_scale.cpu(), pool["vs"])
+    assert torch.equal(c.k.cpu(), pool["k"]) and torch.equal(c.v.cpu(), pool["v"])
+    ko, vo = torch.zeros_like(x), torch.zeros_like(x)
+    P.read(pool, table, [0], [0, T], ko, vo)
+    # (the largest value's scale is rounded up: 127 of its steps are past BF16's range)
+    assert torch.isfinite(ko[:-1].float()).all() and (ko != 0).any(-1).sum() >= T - 5
+    k, v = dv.dvssq_kv_read(c, i32([0]), i32([0, T]), T)
+    assert torch.equal(k.cpu(), ko) and torch.equal(v.cpu(), vo)
