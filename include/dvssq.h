@@ -412,10 +412,11 @@ DVSSQ_API dvssq_status dvssq_bss_attention_q8_workspace_size(const dvssq_attn_sh
  * half a step at most, so that a head of one large value beside small ones
  * keeps few bits of those.  The product of these integers with the codes is
  * exact; logits (NaN past FP32's range), maxima, exponentials and sums (of
- * weights times values, divided at the end) are FP32, and a weight times its value scale enters P V as two BF16 limbs
- * (2^-17 relative).  A key whose weight is zero adds nothing, whatever its
- * value scale holds; a NaN key row makes its KV head's outputs NaN.  tau is
- * at most 1e30.  Results are deterministic.
+ * weights times values, divided at the end) are FP32, and a weight times its
+ * value scale enters P V as two BF16 limbs (2^-17 relative).  A key whose
+ * weight is zero adds nothing, whatever its value scale holds; a NaN key row
+ * makes its KV head's outputs NaN.  tau is at most 1e30.  Results are
+ * deterministic.
  * The kernels are chosen by ctx, not by the lengths: a bound near them (a
  * captured step's: near its longest) is faster than a table's capacity.
  * 17 keys take 5 us under their own bound, 10 us under one of 8192.
